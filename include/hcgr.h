@@ -345,6 +345,203 @@ hcgr_status hcgr_workspace_size_table(const hcgr_config* cfg, const hcgr_plan_ch
  * one handle must not overlap with this one. */
 hcgr_status hcgr_set_plan_table(hcgr_handle h, const hcgr_plan_choice* table, int32_t n);
 
+/* ------------------------------------------------------------------------
+ * The block between two HCGR calls.
+ *
+ * A layer's block (attention, MLP, experts) reads x, projects it, and gives
+ * back y. Around and inside it stand:
+ *   - hcgr_block_norm: the norm before the block, on x;
+ *   - hcgr_linear_quantize, hcgr_linear_forward: its projections as products
+ *     of 8-bit integers, with a scale for each token and each output channel;
+ *   - hcgr_block_residual: the norm after the block, fused with the gates
+ *     that inject y into the HC residual streams, the residual scale and the
+ *     norm before the next block (HC = 1: an ordinary residual stream);
+ * and the gradients of the two norm operators. With norm(v, w)[c] =
+ * v[c] * r * (1 + w[c]), r = 1/sqrt(mean_c v[c]^2 + eps), a token computes
+ *   block_norm      xn = norm(x, w)
+ *   block_residual  z = norm(y, w_post)           (z = y when w_post is NULL)
+ *                   iw[s] = 2*sigmoid(inj[s]/HC)   (1 when inj is NULL)
+ *                   R2[s] = res_scale*R[s] + iw[s]*z
+ *                   x = norm(mean_s R2[s], w_pre)  (absent when w_pre is NULL)
+ *   quantize        q_scale = max_c |v[c]| / 127;
+ *                   q[c] = v[c]/q_scale rounded to the nearest, ties to even
+ *   linear          out[n] = (sum_k q[k]*w[n,k]) * q_scale * w_scale[n] + bias[n]
+ * Sums, norms and gates are held in 32 bits (the linear's sum in 32-bit
+ * integers, exactly); every output is rounded once, from those values. A
+ * quantized output of a norm is taken from the unrounded norm. A row whose
+ * values are all zero quantizes to q = 0, q_scale = 0; a row that holds an
+ * infinity or a NaN to q = 0, q_scale = NaN, so that what is computed from it
+ * is NaN and not a number that looks right. Rows are independent of each
+ * other. Outputs do not depend on timing: the same call gives the same bits.
+ *
+ * Conventions: the ones at the top of this file (host checks first, no
+ * allocation, no synchronisation, capturable, M == 0 returns HCGR_OK and
+ * touches nothing). Tensors of a configuration's dtype are passed as void*.
+ * Leading dimensions (ld_*) count elements. Pointers are aligned to their
+ * element unless stated; when every row of a call starts on a 16-byte
+ * boundary and HS is a whole number of 16-byte pieces, the kernels move
+ * 16 bytes at a time, otherwise one element at a time (slower).
+ * ------------------------------------------------------------------------ */
+#define HCGR_BF16 0
+#define HCGR_FP16 1
+#define HCGR_FP32 2
+
+typedef struct hcgr_block_config {
+    int32_t hc;       /* residual streams: 1, 2, 4 or 8 (hcgr_block_norm does not use it)   */
+    int32_t hs;       /* channels of a stream, 1..65536                                     */
+    int32_t dtype;    /* HCGR_BF16, HCGR_FP16 or HCGR_FP32: type of activations, residual, weights, gates and gradients  */
+    float eps;        /* of both norms (>= 0, finite)                                       */
+    float res_scale;  /* factor on the incoming residual (finite; a constant, no gradient)  */
+} hcgr_block_config;
+
+typedef struct hcgr_block_op* hcgr_block_handle;
+
+/* Validates cfg and binds a handle to `device`; statuses as hcgr_create. The
+ * handle owns host memory only and is read-only afterwards: calls through one
+ * handle may run at the same time on any streams of its device. */
+hcgr_status hcgr_block_create(const hcgr_block_config* cfg, int device, hcgr_block_handle* out);
+void hcgr_block_destroy(hcgr_block_handle h);
+
+/* xn = norm(x, w) for M tokens.
+ *   x       [M, ld_x]   dtype, columns 0..HS-1 read, ld_x >= HS
+ *   w       [HS]        dtype
+ *   xn      [M, HS]     dtype, or NULL
+ *   q       [M, ld_q]   int8, columns 0..HS-1 written, or NULL: the quantized
+ *                       norm; 16-byte aligned, ld_q >= HS and a multiple of 16
+ *                       (the row pitch hcgr_linear_forward reads)
+ *   q_scale [M]         float; given exactly when q is
+ *   rrms    [M]         float, r of each token (the backward pass reads it), or NULL
+ * At least one of xn and q is given. Errors: HCGR_ERR_INVALID_ARGUMENT,
+ * HCGR_ERR_UNSUPPORTED (M > 2^31), HCGR_ERR_ALIASING (an output overlaps an
+ * input or another output), HCGR_ERR_HIP. */
+hcgr_status hcgr_block_norm(hcgr_block_handle h, const void* x, int64_t ld_x, const void* w, int64_t M,
+                            void* xn, int8_t* q, int64_t ld_q, float* q_scale, float* rrms, void* stream);
+
+/* Gradients of xn = norm(x, w): with h = x*r and d = dxn*(1 + w),
+ *   dx = r*(d - h*mean_c(d*h)),   dw = sum_m dxn*h.
+ *   rrms [M] float, from hcgr_block_norm on the same x; dxn [M, HS] dtype;
+ *   dx [M, HS] dtype or NULL; dw [HS] float (summed over the M tokens;
+ *   written, not added to) or NULL; at least one of the two is given.
+ * Workspace: 16-byte aligned, hcgr_block_workspace_size(M) bytes, needs no
+ * initialisation; calls that may run at the same time need separate ones.
+ * Further errors: HCGR_ERR_WORKSPACE_TOO_SMALL. With M == 0 dw, if given, is
+ * not written. */
+hcgr_status hcgr_block_norm_bwd(hcgr_block_handle h, const void* x, int64_t ld_x, const void* w,
+                                const float* rrms, const void* dxn, int64_t M, void* dx, float* dw,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norm after the block, the gated injection, the residual scale and the
+ * next norm for M tokens.
+ *   R       [M, HC*HS]     dtype, streams as in hcgr_forward (s*HS + c)
+ *   y       [M, ld_y]      dtype, columns 0..HS-1 read, ld_y >= HS
+ *   inj     [M, ld_inj]    dtype, columns 0..HC-1 read, ld_inj >= HC; NULL: iw = 1
+ *   w_post  [HS] dtype, or NULL: no norm after the block (z = y)
+ *   w_pre   [HS] dtype, or NULL: no next norm (x and q are NULL then)
+ *   R2      [M, HC*HS]     dtype
+ *   x       [M, HS]        dtype, or NULL
+ *   q, ld_q, q_scale       the next norm quantized, as in hcgr_block_norm, or NULL
+ *   rrms    [M, 2]         float or NULL: r of the norm after the block (column
+ *                          0) and of the next norm (column 1); the column of an
+ *                          absent norm is not written
+ * With w_pre at least one of x and q is given. The next norm is taken from the
+ * unrounded R2. Errors as hcgr_block_norm. */
+hcgr_status hcgr_block_residual(hcgr_block_handle h, const void* R, const void* y, int64_t ld_y,
+                                const void* inj, int64_t ld_inj, const void* w_post, const void* w_pre,
+                                int64_t M, void* R2, void* x, int8_t* q, int64_t ld_q, float* q_scale,
+                                float* rrms, void* stream);
+
+/* Gradients of hcgr_block_residual, from its inputs, its rrms, and the
+ * gradients dR2 [M, HC*HS] (NULL: zero) and dx [M, HS] (given exactly when
+ * w_pre is; a quantized output has no gradient) of its outputs:
+ *   du      = gradient of norm(u, w_pre) in u = mean_s R2[s], from dx
+ *   d[s]    = dR2[s] + du/HC
+ *   dR      [M, HC*HS] = res_scale*d[s]
+ *   dinj    [M, ld_dinj], columns 0..HC-1: (sum_c d[s]*z) * 2*sigmoid'(inj[s]/HC)/HC
+ *   dy      [M, HS]: gradient of norm(y, w_post) from sum_s iw[s]*d[s]
+ *   dw_post, dw_pre [HS] float, summed over the M tokens
+ * dR and dy are always given; dinj exactly when inj is, dw_post when w_post
+ * is, dw_pre when w_pre is; rrms when either norm is present; dR2 or dx or
+ * both. u is formed again from the inputs, unrounded. Workspace and errors as
+ * hcgr_block_norm_bwd; with M == 0 dw_post and dw_pre are not written. */
+hcgr_status hcgr_block_residual_bwd(hcgr_block_handle h, const void* R, const void* y, int64_t ld_y,
+                                    const void* inj, int64_t ld_inj, const void* w_post, const void* w_pre,
+                                    const float* rrms, const void* dR2, const void* dx, int64_t M, void* dR,
+                                    void* dy, void* dinj, int64_t ld_dinj, float* dw_post, float* dw_pre,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes that serve both backward entry points for every token count
+ * from 1 to M (0 for M == 0). The _for form needs no handle (pure host code). */
+hcgr_status hcgr_block_workspace_size(hcgr_block_handle h, int64_t M, size_t* bytes);
+hcgr_status hcgr_block_workspace_size_for(const hcgr_block_config* cfg, int64_t M, size_t* bytes);
+
+/* The host-side checks of the four entry points for a configuration, without
+ * a handle, a device or a launch. Pure host code. */
+hcgr_status hcgr_validate_block_norm(const hcgr_block_config* cfg, const void* x, int64_t ld_x, const void* w,
+                                     int64_t M, const void* xn, const int8_t* q, int64_t ld_q,
+                                     const float* q_scale, const float* rrms);
+hcgr_status hcgr_validate_block_norm_bwd(const hcgr_block_config* cfg, const void* x, int64_t ld_x,
+                                         const void* w, const float* rrms, const void* dxn, int64_t M,
+                                         const void* dx, const float* dw, const void* workspace,
+                                         size_t workspace_bytes);
+hcgr_status hcgr_validate_block_residual(const hcgr_block_config* cfg, const void* R, const void* y,
+                                         int64_t ld_y, const void* inj, int64_t ld_inj, const void* w_post,
+                                         const void* w_pre, int64_t M, const void* R2, const void* x,
+                                         const int8_t* q, int64_t ld_q, const float* q_scale,
+                                         const float* rrms);
+hcgr_status hcgr_validate_block_residual_bwd(const hcgr_block_config* cfg, const void* R, const void* y,
+                                             int64_t ld_y, const void* inj, int64_t ld_inj,
+                                             const void* w_post, const void* w_pre, const float* rrms,
+                                             const void* dR2, const void* dx, int64_t M, const void* dR,
+                                             const void* dy, const void* dinj, int64_t ld_dinj,
+                                             const float* dw_post, const float* dw_pre,
+                                             const void* workspace, size_t workspace_bytes);
+
+/* The 8-bit linear layer. Its sums are exact in 32 bits up to K = 131071
+ * (131071 products of at most 128*128 stay below 2^31). */
+#define HCGR_LINEAR_MAX_K 131071
+#define HCGR_LINEAR_MAX_N 1048576
+#define HCGR_LINEAR_MAX_LD 4194304
+
+typedef struct hcgr_linear_config {
+    int32_t n;      /* output channels, 1..HCGR_LINEAR_MAX_N                        */
+    int32_t k;      /* input channels, 1..HCGR_LINEAR_MAX_K                         */
+    int32_t dtype;  /* HCGR_BF16, HCGR_FP16 or HCGR_FP32: type of hcgr_linear_quantize's input, of out and bias  */
+} hcgr_linear_config;
+
+typedef struct hcgr_linear_op* hcgr_linear_handle;
+
+/* As hcgr_block_create / hcgr_block_destroy. */
+hcgr_status hcgr_linear_create(const hcgr_linear_config* cfg, int device, hcgr_linear_handle* out);
+void hcgr_linear_destroy(hcgr_linear_handle h);
+
+/* Quantizes M rows of K values: activations (a row a token) before
+ * hcgr_linear_forward, or a weight matrix (M = N, a row an output channel).
+ *   x [M, ld_x] dtype, ld_x >= K; q [M, ld_q] int8, columns 0..K-1 written,
+ *   16-byte aligned, ld_q >= K and a multiple of 16; q_scale [M] float. */
+hcgr_status hcgr_linear_quantize(hcgr_linear_handle h, const void* x, int64_t ld_x, int64_t M, int8_t* q,
+                                 int64_t ld_q, float* q_scale, void* stream);
+
+/* out[m, n] = (sum_k q[m, k]*w[n, k]) * q_scale[m] * w_scale[n] + bias[n].
+ *   q [M, ld_q] and w [N, ld_w] int8 (any of the 256 values), 16-byte
+ *   aligned, leading dimensions multiples of 16, >= K and at most
+ *   HCGR_LINEAR_MAX_LD. Each row is read in whole 16-byte pieces: the bytes of
+ *   a row's last piece past K, in the last row too, must be readable and are
+ *   ignored.
+ *   q_scale [M], w_scale [N] float; bias [N] dtype or NULL;
+ *   out [M, ld_out] dtype, columns 0..N-1 written, ld_out >= N.
+ * Needs no workspace. Errors as hcgr_block_norm. */
+hcgr_status hcgr_linear_forward(hcgr_linear_handle h, const int8_t* q, int64_t ld_q, const float* q_scale,
+                                const int8_t* w, int64_t ld_w, const float* w_scale, const void* bias,
+                                int64_t M, void* out, int64_t ld_out, void* stream);
+
+/* Host-side checks, as hcgr_validate_block_norm. */
+hcgr_status hcgr_validate_linear_quantize(const hcgr_linear_config* cfg, const void* x, int64_t ld_x,
+                                          int64_t M, const int8_t* q, int64_t ld_q, const float* q_scale);
+hcgr_status hcgr_validate_linear_forward(const hcgr_linear_config* cfg, const int8_t* q, int64_t ld_q,
+                                         const float* q_scale, const int8_t* w, int64_t ld_w,
+                                         const float* w_scale, const void* bias, int64_t M, const void* out,
+                                         int64_t ld_out);
+
 /* Static name of a status code. */
 const char* hcgr_status_string(hcgr_status s);
 

@@ -34,6 +34,12 @@ HCGR_PLAN_FUSED = 4
 HCGR_PLAN_PERSISTENT = 5
 HCGR_SPLIT_VARIANTS = 13  # down-kernel variants of the decode plans (include/hcgr.h)
 HCGR_WORKSPACE_COUNTER_BYTES = 131072
+HCGR_BF16 = 0
+HCGR_FP16 = 1
+HCGR_FP32 = 2
+HCGR_LINEAR_MAX_K = 131071
+HCGR_LINEAR_MAX_N = 1048576
+HCGR_LINEAR_MAX_LD = 4194304
 HCGR_DEFAULT_WAIT_POLLS = 1 << 20
 HCGR_MAX_WAIT_POLLS = 1 << 24
 PLAN_FIELDS = ("tokens", "kind", "down_variant", "streams_per_wg", "segments", "up_variant", "ranges")
@@ -49,6 +55,15 @@ class hcgr_config(ctypes.Structure):
     _fields_ = [("hc", ctypes.c_int32), ("hs", ctypes.c_int32), ("r", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("wnorm_len", ctypes.c_int32),
                 ("weight_layout", ctypes.c_int32), ("n_pad", ctypes.c_int32)]
+
+
+class hcgr_block_config(ctypes.Structure):
+    _fields_ = [("hc", ctypes.c_int32), ("hs", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float)]
+
+
+class hcgr_linear_config(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class hcgr_plan_choice(ctypes.Structure):
@@ -94,6 +109,35 @@ class Config:
         return self.weight_layout == HCGR_WEIGHTS_MERGED_FOLDED
 
 
+@dataclass(frozen=True)
+class BlockConfig:
+    """Streams, width, type and constants of the norms around a block
+    (``hcgr_block_config``)."""
+    hc: int = 4
+    hs: int = 2560
+    dtype: int = HCGR_BF16
+    eps: float = 1e-6
+    res_scale: float = 1.0
+
+    def c(self) -> hcgr_block_config:
+        return hcgr_block_config(self.hc, self.hs, self.dtype, self.eps, self.res_scale)
+
+    @property
+    def k(self) -> int:
+        return self.hc * self.hs
+
+
+@dataclass(frozen=True)
+class LinearConfig:
+    """Sizes of an 8-bit linear layer and the type around it (``hcgr_linear_config``)."""
+    n: int
+    k: int
+    dtype: int = HCGR_BF16
+
+    def c(self) -> hcgr_linear_config:
+        return hcgr_linear_config(self.n, self.k, self.dtype)
+
+
 _lib = None
 
 
@@ -131,6 +175,25 @@ def load_library(path: str = LIB_PATH):
     lib.hcgr_workspace_size_table.argtypes = [CFG, PC, ctypes.c_int32, I64, ctypes.POINTER(SZ)]
     lib.hcgr_set_plan_table.argtypes = [P, PC, ctypes.c_int32]
     lib.hcgr_set_wait_polls.argtypes = [P, ctypes.c_int32]
+    BCFG, LCFG = ctypes.POINTER(hcgr_block_config), ctypes.POINTER(hcgr_linear_config)
+    block = {"norm": [P, I64, P, I64, P, P, I64, P, P],
+             "norm_bwd": [P, I64, P, P, P, I64, P, P, P, SZ],
+             "residual": [P, P, I64, P, I64, P, P, I64, P, P, P, I64, P, P],
+             "residual_bwd": [P, P, I64, P, I64, P, P, P, P, P, I64, P, P, P, I64, P, P, P, SZ]}
+    linear = {"quantize": [P, I64, I64, P, I64, P],
+              "forward": [P, I64, P, P, I64, P, P, I64, P, I64]}
+    added = ["hcgr_block_create", "hcgr_block_workspace_size", "hcgr_block_workspace_size_for", "hcgr_linear_create"]
+    lib.hcgr_block_create.argtypes = [BCFG, ctypes.c_int, ctypes.POINTER(P)]
+    lib.hcgr_linear_create.argtypes = [LCFG, ctypes.c_int, ctypes.POINTER(P)]
+    lib.hcgr_block_destroy.argtypes = lib.hcgr_linear_destroy.argtypes = [P]
+    lib.hcgr_block_destroy.restype = lib.hcgr_linear_destroy.restype = None
+    lib.hcgr_block_workspace_size.argtypes = [P, I64, ctypes.POINTER(SZ)]
+    lib.hcgr_block_workspace_size_for.argtypes = [BCFG, I64, ctypes.POINTER(SZ)]
+    for kind, cfg, calls in (("block", BCFG, block), ("linear", LCFG, linear)):
+        for name, args in calls.items():
+            getattr(lib, f"hcgr_{kind}_{name}").argtypes = [P, *args, P]
+            getattr(lib, f"hcgr_validate_{kind}_{name}").argtypes = [cfg, *args]
+            added += [f"hcgr_{kind}_{name}", f"hcgr_validate_{kind}_{name}"]
     lib.hcgr_status_string.argtypes = [ctypes.c_int]
     lib.hcgr_status_string.restype = ctypes.c_char_p
     lib.hcgr_last_error.argtypes = []
@@ -138,7 +201,8 @@ def load_library(path: str = LIB_PATH):
     for name in ("hcgr_create", "hcgr_workspace_size", "hcgr_workspace_size_for", "hcgr_forward",
                  "hcgr_forward_timed", "hcgr_forward_noalloc", "hcgr_combine", "hcgr_mix", "hcgr_validate_combine",
                  "hcgr_validate_mix", "hcgr_validate", "hcgr_describe_plan", "hcgr_plan_candidates",
-                 "hcgr_plan_lookup", "hcgr_workspace_size_table", "hcgr_set_plan_table", "hcgr_set_wait_polls"):
+                 "hcgr_plan_lookup", "hcgr_workspace_size_table", "hcgr_set_plan_table", "hcgr_set_wait_polls",
+                 *added):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -361,6 +425,135 @@ def hcgr_validate(cfg: Config, R, y, inj, ld_inj, wnorm, wd, wi, wu, M, R2, rrms
                                         int(ld_inj_next), _p(x), _p(workspace), int(workspace_bytes))
 
 
+# ---------------------------------------- the block operators, same names --
+def hcgr_block_create(cfg: BlockConfig, device: int = 0) -> int:
+    h, c = ctypes.c_void_p(), cfg.c()
+    _check(load_library().hcgr_block_create(ctypes.byref(c), int(device), ctypes.byref(h)), "hcgr_block_create")
+    return h.value
+
+
+def hcgr_block_destroy(handle: int) -> None:
+    load_library().hcgr_block_destroy(handle)
+
+
+def hcgr_block_workspace_size(handle: int, M: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().hcgr_block_workspace_size(handle, int(M), ctypes.byref(n)), "hcgr_block_workspace_size")
+    return n.value
+
+
+def hcgr_block_workspace_size_for(cfg: BlockConfig, M: int) -> int:
+    n, c = ctypes.c_size_t(), cfg.c()
+    _check(load_library().hcgr_block_workspace_size_for(ctypes.byref(c), int(M), ctypes.byref(n)),
+           "hcgr_block_workspace_size_for")
+    return n.value
+
+
+def _call(name, handle, args, stream, like, check):
+    st = getattr(load_library(), name)(handle, *args, _stream(stream, like))
+    if check:
+        _check(st, name)
+    return st
+
+
+def _validate(name, cfg, args):
+    c = cfg.c()
+    return getattr(load_library(), name)(ctypes.byref(c), *args)
+
+
+def _norm_args(x, ld_x, w, M, xn, q, ld_q, q_scale, rrms):
+    return _p(x), int(ld_x), _p(w), int(M), _p(xn), _p(q), int(ld_q), _p(q_scale), _p(rrms)
+
+
+def _norm_bwd_args(x, ld_x, w, rrms, dxn, M, dx, dw, workspace, workspace_bytes):
+    return (_p(x), int(ld_x), _p(w), _p(rrms), _p(dxn), int(M), _p(dx), _p(dw), _p(workspace), int(workspace_bytes))
+
+
+def _residual_args(R, y, ld_y, inj, ld_inj, w_post, w_pre, M, R2, x, q, ld_q, q_scale, rrms):
+    return (_p(R), _p(y), int(ld_y), _p(inj), int(ld_inj), _p(w_post), _p(w_pre), int(M), _p(R2), _p(x), _p(q),
+            int(ld_q), _p(q_scale), _p(rrms))
+
+
+def _residual_bwd_args(R, y, ld_y, inj, ld_inj, w_post, w_pre, rrms, dR2, dx, M, dR, dy, dinj, ld_dinj, dw_post,
+                       dw_pre, workspace, workspace_bytes):
+    return (_p(R), _p(y), int(ld_y), _p(inj), int(ld_inj), _p(w_post), _p(w_pre), _p(rrms), _p(dR2), _p(dx), int(M),
+            _p(dR), _p(dy), _p(dinj), int(ld_dinj), _p(dw_post), _p(dw_pre), _p(workspace), int(workspace_bytes))
+
+
+def _quantize_args(x, ld_x, M, q, ld_q, q_scale):
+    return _p(x), int(ld_x), int(M), _p(q), int(ld_q), _p(q_scale)
+
+
+def _linear_args(q, ld_q, q_scale, w, ld_w, w_scale, bias, M, out, ld_out):
+    return (_p(q), int(ld_q), _p(q_scale), _p(w), int(ld_w), _p(w_scale), _p(bias), int(M), _p(out), int(ld_out))
+
+
+def hcgr_block_norm(handle, x, *args, stream=None, check: bool = True) -> int:
+    """(x, ld_x, w, M, xn, q, ld_q, q_scale, rrms); stream as in ``hcgr_forward``."""
+    return _call("hcgr_block_norm", handle, _norm_args(x, *args), stream, x, check)
+
+
+def hcgr_block_norm_bwd(handle, x, *args, stream=None, check: bool = True) -> int:
+    """(x, ld_x, w, rrms, dxn, M, dx, dw, workspace, workspace_bytes)."""
+    return _call("hcgr_block_norm_bwd", handle, _norm_bwd_args(x, *args), stream, x, check)
+
+
+def hcgr_block_residual(handle, R, *args, stream=None, check: bool = True) -> int:
+    """(R, y, ld_y, inj, ld_inj, w_post, w_pre, M, R2, x, q, ld_q, q_scale, rrms)."""
+    return _call("hcgr_block_residual", handle, _residual_args(R, *args), stream, R, check)
+
+
+def hcgr_block_residual_bwd(handle, R, *args, stream=None, check: bool = True) -> int:
+    """(R, y, ld_y, inj, ld_inj, w_post, w_pre, rrms, dR2, dx, M, dR, dy, dinj,
+    ld_dinj, dw_post, dw_pre, workspace, workspace_bytes)."""
+    return _call("hcgr_block_residual_bwd", handle, _residual_bwd_args(R, *args), stream, R, check)
+
+
+def hcgr_validate_block_norm(cfg: BlockConfig, *args) -> int:
+    """Host-only checks of ``hcgr_block_norm``; returns the status code (does not raise)."""
+    return _validate("hcgr_validate_block_norm", cfg, _norm_args(*args))
+
+
+def hcgr_validate_block_norm_bwd(cfg: BlockConfig, *args) -> int:
+    return _validate("hcgr_validate_block_norm_bwd", cfg, _norm_bwd_args(*args))
+
+
+def hcgr_validate_block_residual(cfg: BlockConfig, *args) -> int:
+    return _validate("hcgr_validate_block_residual", cfg, _residual_args(*args))
+
+
+def hcgr_validate_block_residual_bwd(cfg: BlockConfig, *args) -> int:
+    return _validate("hcgr_validate_block_residual_bwd", cfg, _residual_bwd_args(*args))
+
+
+def hcgr_linear_create(cfg: LinearConfig, device: int = 0) -> int:
+    h, c = ctypes.c_void_p(), cfg.c()
+    _check(load_library().hcgr_linear_create(ctypes.byref(c), int(device), ctypes.byref(h)), "hcgr_linear_create")
+    return h.value
+
+
+def hcgr_linear_destroy(handle: int) -> None:
+    load_library().hcgr_linear_destroy(handle)
+
+
+def hcgr_linear_quantize(handle, x, *args, stream=None, check: bool = True) -> int:
+    """(x, ld_x, M, q, ld_q, q_scale)."""
+    return _call("hcgr_linear_quantize", handle, _quantize_args(x, *args), stream, x, check)
+
+
+def hcgr_linear_forward(handle, q, *args, stream=None, check: bool = True) -> int:
+    """(q, ld_q, q_scale, w, ld_w, w_scale, bias, M, out, ld_out)."""
+    return _call("hcgr_linear_forward", handle, _linear_args(q, *args), stream, q, check)
+
+
+def hcgr_validate_linear_quantize(cfg: LinearConfig, *args) -> int:
+    return _validate("hcgr_validate_linear_quantize", cfg, _quantize_args(*args))
+
+
+def hcgr_validate_linear_forward(cfg: LinearConfig, *args) -> int:
+    return _validate("hcgr_validate_linear_forward", cfg, _linear_args(*args))
+
+
 def new_workspace(nbytes: int, device: int = 0):
     """A zero-filled device workspace of at least nbytes (the counter bytes at
     its start must be zero before the first call that uses it)."""
@@ -456,4 +649,275 @@ class HCGR:
         ld = inj.stride(0) if ld_inj is None else ld_inj
         hcgr_forward(self.handle, R, y, inj, ld, wnorm, wd, wi, wu, M, out["R2"], out["rrms"],
                      out["inj_next"], out["ld_inj_next"], out["x"], ws, ws.numel(), stream)
+        return out
+
+
+def torch_dtype(dtype: int):
+    """The torch type of an HCGR_BF16, HCGR_FP16 or HCGR_FP32 configuration."""
+    import torch
+    return {HCGR_BF16: torch.bfloat16, HCGR_FP16: torch.float16, HCGR_FP32: torch.float32}[dtype]
+
+
+def _round16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+class _Op:
+    """What ``Block`` and ``Int8Linear`` share: the handle, argument checks (a
+    tensor of another type, shape or device raises ValueError before any
+    launch) and outputs that may be used on another stream than torch's."""
+
+    def __init__(self, cfg, device: int, create, destroy):
+        import torch
+        self.cfg, self.device = cfg, int(device)
+        self._destroy = destroy
+        self.handle = create(cfg, self.device)
+        self.dtype = torch_dtype(cfg.dtype)
+        self._torch = torch
+        self._lib = load_library()
+
+    def close(self):
+        if getattr(self, "handle", None):
+            self._destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _bad(self, name, t, want):
+        got = f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" if hasattr(t, "dtype") else repr(t)
+        raise ValueError(f"{name}: expected {want} on cuda:{self.device}, got {got}")
+
+    def _dense(self, name, t, dtype, shape):
+        """Address of a contiguous tensor of this type and shape, None for None."""
+        if t is None:
+            return None
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.device or not t.is_contiguous():
+            self._bad(name, t, f"contiguous {dtype} {tuple(shape)}")
+        return t.data_ptr()
+
+    def _rows(self, name, t, dtype, m, cols):
+        """Address and row pitch of a matrix whose rows are contiguous."""
+        if t.dtype is not dtype or t.shape != (m, cols) or t.get_device() != self.device or \
+                (cols > 1 and t.stride(1) != 1):
+            self._bad(name, t, f"{dtype} {(m, cols)} with contiguous rows")
+        return t.data_ptr(), t.stride(0) if m > 1 else cols
+
+    def _rows8(self, name, t, m, cols):
+        """The same for int8 rows, which are read in whole 16-byte pieces."""
+        p, ld = self._rows(name, t, self._torch.int8, m, cols)
+        if m == 1:
+            ld = _round16(cols)
+        if m and cols % 16 and t.untyped_storage().nbytes() < t.storage_offset() + (m - 1) * ld + _round16(cols):
+            raise ValueError(f"{name}: rows of {cols} int8 need a pitch of whole 16-byte pieces "
+                             "(alloc_quantized makes such rows)")
+        return p, ld
+
+    def _raw(self, stream):
+        if stream is None:
+            return self._torch.cuda.current_stream(self.device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _made(self, stream, *tensors):
+        """Tensors allocated here and used on `stream`: torch must not hand
+        their memory on before that stream is done with them."""
+        if stream is None:
+            return
+        cuda = self._torch.cuda
+        s = cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+        if s != cuda.current_stream(self.device):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+
+    def _empty(self, shape, dtype):
+        return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
+
+    def _quantized(self, m, cols):
+        """int8 [m, cols] at a pitch of whole 16-byte pieces, and its scales."""
+        return self._empty((m, _round16(cols)), self._torch.int8)[:, :cols], self._empty((m,), self._torch.float32)
+
+
+class Block(_Op):
+    """The norms around a block and their gradients (``hcgr_block_*``), with
+    outputs and workspaces allocated by torch. ``out`` takes a dict of an
+    ``alloc_*`` method (or of an earlier call) and is returned."""
+
+    def __init__(self, cfg: BlockConfig = BlockConfig(), device: int = 0):
+        super().__init__(cfg, device, hcgr_block_create, hcgr_block_destroy)
+
+    def alloc_norm(self, M: int, *, quantize: bool = False, keep: bool = False) -> dict:
+        """``quantize``: q and q_scale in place of x; ``keep``: x as well."""
+        f32, hs = self._torch.float32, self.cfg.hs
+        out = {"rrms": self._empty((M,), f32)}
+        if quantize:
+            out["q"], out["q_scale"] = self._quantized(M, hs)
+        if keep or not quantize:
+            out["x"] = self._empty((M, hs), self.dtype)
+        return out
+
+    def alloc_norm_bwd(self, M: int) -> dict:
+        return {"dx": self._empty((M, self.cfg.hs), self.dtype), "dw": self._empty((self.cfg.hs,), self._torch.float32)}
+
+    def alloc_residual(self, M: int, *, norm: bool = True, quantize: bool = False, keep: bool = False) -> dict:
+        """``norm``: the next norm is wanted (w_pre is given)."""
+        out = self.alloc_norm(M, quantize=quantize, keep=keep) if norm else {}
+        out["rrms"] = self._empty((M, 2), self._torch.float32)
+        out["R2"] = self._empty((M, self.cfg.k), self.dtype)
+        return out
+
+    def alloc_residual_bwd(self, M: int, *, gates: bool = True, post: bool = True, pre: bool = True) -> dict:
+        c, f32 = self.cfg, self._torch.float32
+        out = {"dR": self._empty((M, c.k), self.dtype), "dy": self._empty((M, c.hs), self.dtype)}
+        if gates:
+            out["dinj"] = self._empty((M, c.hc), self.dtype)
+        if post:
+            out["dw_post"] = self._empty((c.hs,), f32)
+        if pre:
+            out["dw_pre"] = self._empty((c.hs,), f32)
+        return out
+
+    def workspace(self, M: int):
+        """A workspace for the backward entry points (no initialisation needed)."""
+        return self._empty((hcgr_block_workspace_size(self.handle, M),), self._torch.uint8)
+
+    def _norm_outputs(self, out, M):
+        hs, f32 = self.cfg.hs, self._torch.float32
+        x = self._dense("x", out.get("x"), self.dtype, (M, hs))
+        q, ld_q, qs = out.get("q"), 0, None
+        if q is not None:
+            q, ld_q = self._rows8("q", q, M, hs)
+            qs = self._dense("q_scale", out["q_scale"], f32, (M,))
+        return x, q, ld_q, qs
+
+    def _ws(self, workspace, M):
+        if workspace is None:
+            return self.workspace(M)
+        if workspace.dtype is not self._torch.uint8 or workspace.get_device() != self.device or \
+                not workspace.is_contiguous():
+            self._bad("workspace", workspace, "contiguous uint8")
+        return workspace
+
+    def norm(self, x, w, *, quantize: bool = False, out: dict | None = None, stream=None) -> dict:
+        """x [M, HS] (rows may be strided) -> x or (q, q_scale), and rrms."""
+        M, hs = x.shape[0], self.cfg.hs
+        px, ld_x = self._rows("x", x, self.dtype, M, hs)
+        if out is None:
+            out = self.alloc_norm(M, quantize=quantize)
+            self._made(stream, *out.values())
+        xn, q, ld_q, qs = self._norm_outputs(out, M)
+        _check(self._lib.hcgr_block_norm(
+            self.handle, px, ld_x, self._dense("w", w, self.dtype, (hs,)), M, xn, q, ld_q, qs,
+            self._dense("rrms", out.get("rrms"), self._torch.float32, (M,)), self._raw(stream)), "hcgr_block_norm")
+        return out
+
+    def norm_bwd(self, x, w, rrms, dxn, *, out: dict | None = None, workspace=None, stream=None) -> dict:
+        """Gradients dx [M, HS] and dw [HS] (float32, summed over the tokens) of ``norm``."""
+        M, hs, f32 = x.shape[0], self.cfg.hs, self._torch.float32
+        px, ld_x = self._rows("x", x, self.dtype, M, hs)
+        if out is None:
+            out = self.alloc_norm_bwd(M)
+            self._made(stream, *out.values())
+        ws = self._ws(workspace, M)
+        if workspace is None:
+            self._made(stream, ws)
+        _check(self._lib.hcgr_block_norm_bwd(
+            self.handle, px, ld_x, self._dense("w", w, self.dtype, (hs,)), self._dense("rrms", rrms, f32, (M,)),
+            self._dense("dxn", dxn, self.dtype, (M, hs)), M, self._dense("dx", out.get("dx"), self.dtype, (M, hs)),
+            self._dense("dw", out.get("dw"), f32, (hs,)), ws.data_ptr(), ws.numel(), self._raw(stream)),
+            "hcgr_block_norm_bwd")
+        return out
+
+    def residual(self, R, y, inj=None, w_post=None, w_pre=None, *, quantize: bool = False, out: dict | None = None,
+                 stream=None) -> dict:
+        """R [M, HC*HS], y [M, HS], inj [M, HC] (rows of y and inj may be strided)
+        -> R2, rrms, and with w_pre the next norm as x or (q, q_scale)."""
+        c, dt = self.cfg, self.dtype
+        M, hs, k = R.shape[0], c.hs, c.hc * c.hs
+        py, ld_y = self._rows("y", y, dt, M, hs)
+        pi, ld_i = self._rows("inj", inj, dt, M, c.hc) if inj is not None else (None, 0)
+        if out is None:
+            out = self.alloc_residual(M, norm=w_pre is not None, quantize=quantize)
+            self._made(stream, *out.values())
+        x, q, ld_q, qs = self._norm_outputs(out, M)
+        _check(self._lib.hcgr_block_residual(
+            self.handle, self._dense("R", R, dt, (M, k)), py, ld_y, pi, ld_i,
+            self._dense("w_post", w_post, dt, (hs,)), self._dense("w_pre", w_pre, dt, (hs,)), M,
+            self._dense("R2", out["R2"], dt, (M, k)), x, q, ld_q, qs,
+            self._dense("rrms", out.get("rrms"), self._torch.float32, (M, 2)), self._raw(stream)),
+            "hcgr_block_residual")
+        return out
+
+    def residual_bwd(self, R, y, inj, w_post, w_pre, rrms, dR2, dx, *, out: dict | None = None, workspace=None,
+                     stream=None) -> dict:
+        """Gradients dR, dy, dinj, dw_post and dw_pre (those whose input is
+        given) of ``residual`` from dR2 [M, HC*HS] and dx [M, HS]."""
+        c, dt, f32 = self.cfg, self.dtype, self._torch.float32
+        M, hs, k = R.shape[0], c.hs, c.hc * c.hs
+        py, ld_y = self._rows("y", y, dt, M, hs)
+        pi, ld_i = self._rows("inj", inj, dt, M, c.hc) if inj is not None else (None, 0)
+        if out is None:
+            out = self.alloc_residual_bwd(M, gates=inj is not None, post=w_post is not None, pre=w_pre is not None)
+            self._made(stream, *out.values())
+        di, ld_di = out.get("dinj"), 0
+        if di is not None:
+            di, ld_di = self._rows("dinj", di, dt, M, c.hc)
+        ws = self._ws(workspace, M)
+        if workspace is None:
+            self._made(stream, ws)
+        _check(self._lib.hcgr_block_residual_bwd(
+            self.handle, self._dense("R", R, dt, (M, k)), py, ld_y, pi, ld_i,
+            self._dense("w_post", w_post, dt, (hs,)), self._dense("w_pre", w_pre, dt, (hs,)),
+            self._dense("rrms", rrms, f32, (M, 2)), self._dense("dR2", dR2, dt, (M, k)),
+            self._dense("dx", dx, dt, (M, hs)), M, self._dense("dR", out["dR"], dt, (M, k)),
+            self._dense("dy", out["dy"], dt, (M, hs)), di, ld_di, self._dense("dw_post", out.get("dw_post"), f32, (hs,)),
+            self._dense("dw_pre", out.get("dw_pre"), f32, (hs,)), ws.data_ptr(), ws.numel(), self._raw(stream)),
+            "hcgr_block_residual_bwd")
+        return out
+
+
+class Int8Linear(_Op):
+    """An 8-bit linear layer [K] -> [N] (``hcgr_linear_*``). Weights are the
+    caller's: int8 [N, K] with a float32 scale for each output channel, as
+    ``quantize`` makes them from a float matrix."""
+
+    def __init__(self, cfg: LinearConfig, device: int = 0):
+        super().__init__(cfg, device, hcgr_linear_create, hcgr_linear_destroy)
+
+    def alloc_quantized(self, M: int):
+        """(q, q_scale) for M rows of K values, q at a pitch of whole 16-byte pieces."""
+        return self._quantized(M, self.cfg.k)
+
+    def alloc_output(self, M: int):
+        return self._empty((M, self.cfg.n), self.dtype)
+
+    def quantize(self, x, *, out=None, stream=None):
+        """Rows [M, K] (tokens, or a weight's output channels) -> (q, q_scale)."""
+        M, k = x.shape[0], self.cfg.k
+        px, ld_x = self._rows("x", x, self.dtype, M, k)
+        if out is None:
+            out = self.alloc_quantized(M)
+            self._made(stream, *out)
+        q, ld_q = self._rows8("q", out[0], M, k)
+        _check(self._lib.hcgr_linear_quantize(
+            self.handle, px, ld_x, M, q, ld_q, self._dense("q_scale", out[1], self._torch.float32, (M,)),
+            self._raw(stream)), "hcgr_linear_quantize")
+        return out
+
+    def forward(self, q, q_scale, w, w_scale, bias=None, *, out=None, stream=None):
+        """out [M, N] from tokens q int8 [M, K] and weights w int8 [N, K]."""
+        c, f32, M = self.cfg, self._torch.float32, q.shape[0]
+        pq, ld_q = self._rows8("q", q, M, c.k)
+        pw, ld_w = self._rows8("w", w, c.n, c.k)
+        if out is None:
+            out = self.alloc_output(M)
+            self._made(stream, out)
+        po, ld_o = self._rows("out", out, self.dtype, M, c.n)
+        _check(self._lib.hcgr_linear_forward(
+            self.handle, pq, ld_q, self._dense("q_scale", q_scale, f32, (M,)), pw, ld_w,
+            self._dense("w_scale", w_scale, f32, (c.n,)), self._dense("bias", bias, self.dtype, (c.n,)), M, po, ld_o,
+            self._raw(stream)), "hcgr_linear_forward")
         return out

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/hcgr.h"
+#include "hcgr_host.h"
 #include "hcgr_internal.h"
 
 struct hcgr_op {
@@ -40,7 +41,10 @@ void* g_scratch[kMaxDevices] = {};
 
 thread_local char g_err[512] = "";
 
-hcgr_status fail(hcgr_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+namespace hcgr_host {
+
 hcgr_status fail(hcgr_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -53,6 +57,75 @@ hcgr_status ok() {
   g_err[0] = '\0';
   return HCGR_OK;
 }
+
+hcgr_status check_overlaps(const Range* outs, int nout, const Range* ins, int nin) {
+  for (int i = 0; i < nout; ++i) {
+    if (outs[i].hi == outs[i].lo) continue;  // not part of this call
+    for (int j = i + 1; j < nout; ++j)
+      if (outs[j].hi > outs[j].lo && overlap(outs[i], outs[j]))
+        return fail(HCGR_ERR_ALIASING, "output %s overlaps output %s", outs[i].name, outs[j].name);
+    for (int j = 0; j < nin; ++j)
+      if (ins[j].hi > ins[j].lo && overlap(outs[i], ins[j]))
+        return fail(HCGR_ERR_ALIASING, "output %s overlaps input %s", outs[i].name, ins[j].name);
+  }
+  return HCGR_OK;
+}
+
+hcgr_status check_ptrs(const PtrCheck* ptrs, int n) {
+  for (int i = 0; i < n; ++i) {
+    const PtrCheck& p = ptrs[i];
+    if (!p.p) return fail(HCGR_ERR_INVALID_ARGUMENT, "%s is NULL", p.name);
+    if ((uintptr_t)p.p % p.align) return fail(HCGR_ERR_INVALID_ARGUMENT, "%s is not %zu-byte aligned", p.name, p.align);
+  }
+  return HCGR_OK;
+}
+
+hcgr_status check_device(int device) {
+  int ndev = 0;
+  hipError_t e = hipGetDeviceCount(&ndev);
+  if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDeviceCount: %s", hipGetErrorString(e));
+  if (device < 0 || device >= ndev)
+    return fail(HCGR_ERR_INVALID_ARGUMENT, "device %d out of range (%d devices)", device, ndev);
+  hipDeviceProp_t prop;
+  e = hipGetDeviceProperties(&prop, device);
+  if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDeviceProperties: %s", hipGetErrorString(e));
+  if (strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+    return fail(HCGR_ERR_UNSUPPORTED, "device %d is %s; the kernels are built for gfx950 (MI355X)", device,
+                prop.gcnArchName);
+  return HCGR_OK;
+}
+
+hcgr_status enter_device(int device, void* stream, int* prev) {
+  int dev = -1;
+  hipError_t e;
+  if (stream) {
+    e = hipStreamGetDevice(reinterpret_cast<hipStream_t>(stream), &dev);
+    if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipStreamGetDevice: %s", hipGetErrorString(e));
+  } else {
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
+  }
+  if (dev != device)
+    return fail(HCGR_ERR_INVALID_ARGUMENT, "stream belongs to device %d, handle to device %d", dev, device);
+  int cur = -1;
+  e = hipGetDevice(&cur);
+  if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
+  if (cur != device) {
+    e = hipSetDevice(device);
+    if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipSetDevice: %s", hipGetErrorString(e));
+  }
+  *prev = cur;
+  return HCGR_OK;
+}
+void restore_device(int device, int prev) {
+  if (prev != device) (void)hipSetDevice(prev);
+}
+
+}  // namespace hcgr_host
+
+namespace {
+
+using namespace hcgr_host;
 
 // Config checks shared by create, validate and the size queries.
 hcgr_status check_config(const hcgr_config* c, hcgr::Shape* out) {
@@ -83,28 +156,6 @@ hcgr_status check_config(const hcgr_config* c, hcgr::Shape* out) {
     out->wn_full = (int64_t)c->wnorm_len == k && c->wnorm_len != c->hs;
     out->merged = c->weight_layout == HCGR_WEIGHTS_MERGED_FOLDED;
     out->n_pad = c->n_pad;
-  }
-  return HCGR_OK;
-}
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-  const char* name;
-};
-
-bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
-
-struct PtrCheck {
-  const void* p;
-  const char* name;
-  size_t align;
-};
-
-hcgr_status check_ptrs(const PtrCheck* ptrs, int n) {
-  for (int i = 0; i < n; ++i) {
-    const PtrCheck& p = ptrs[i];
-    if (!p.p) return fail(HCGR_ERR_INVALID_ARGUMENT, "%s is NULL", p.name);
-    if ((uintptr_t)p.p % p.align) return fail(HCGR_ERR_INVALID_ARGUMENT, "%s is not %zu-byte aligned", p.name, p.align);
   }
   return HCGR_OK;
 }
@@ -169,15 +220,7 @@ hcgr_status check_forward(const hcgr_config* cfg, const hcgr::Shape& s, const ui
       rng(ws, plan.ws_bytes, "workspace"),
   };
   const int nin = sizeof ins / sizeof ins[0], nout = sizeof outs / sizeof outs[0];
-  for (int i = 0; i < nout; ++i) {
-    if (outs[i].hi == outs[i].lo) continue;  // not part of this call
-    for (int j = i + 1; j < nout; ++j)
-      if (outs[j].hi > outs[j].lo && overlap(outs[i], outs[j]))
-        return fail(HCGR_ERR_ALIASING, "output %s overlaps output %s", outs[i].name, outs[j].name);
-    for (int j = 0; j < nin; ++j)
-      if (ins[j].hi > ins[j].lo && overlap(outs[i], ins[j]))
-        return fail(HCGR_ERR_ALIASING, "output %s overlaps input %s", outs[i].name, ins[j].name);
-  }
+  if ((pst = check_overlaps(outs, nout, ins, nin)) != HCGR_OK) return pst;
   if (plan_out) *plan_out = plan;
   return ok();
 }
@@ -410,17 +453,10 @@ hcgr_status hcgr_create(const hcgr_config* cfg, int device, hcgr_handle* out) {
   hcgr::Shape s;
   hcgr_status st = check_config(cfg, &s);
   if (st != HCGR_OK) return st;
-  int ndev = 0;
-  hipError_t e = hipGetDeviceCount(&ndev);
-  if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDeviceCount: %s", hipGetErrorString(e));
-  if (device < 0 || device >= ndev)
-    return fail(HCGR_ERR_INVALID_ARGUMENT, "device %d out of range (%d devices)", device, ndev);
+  if ((st = check_device(device)) != HCGR_OK) return st;
   hipDeviceProp_t prop;
-  e = hipGetDeviceProperties(&prop, device);
+  hipError_t e = hipGetDeviceProperties(&prop, device);
   if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDeviceProperties: %s", hipGetErrorString(e));
-  if (strncmp(prop.gcnArchName, "gfx950", 6) != 0)
-    return fail(HCGR_ERR_UNSUPPORTED, "device %d is %s; the kernels are built for gfx950 (MI355X)", device,
-                prop.gcnArchName);
   int cur = -1;
   e = hipGetDevice(&cur);
   if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
@@ -472,34 +508,6 @@ hcgr_status hcgr_validate(const hcgr_config* cfg, const uint16_t* R, const uint1
                        workspace, workspace_bytes, nullptr);
 }
 
-// Stream and device checks shared by every launching entry point; on success
-// *prev is the caller's current device (restore it with restore_device).
-static hcgr_status enter_device(hcgr_handle h, void* stream, int* prev) {
-  int dev = -1;
-  hipError_t e;
-  if (stream) {
-    e = hipStreamGetDevice(reinterpret_cast<hipStream_t>(stream), &dev);
-    if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipStreamGetDevice: %s", hipGetErrorString(e));
-  } else {
-    e = hipGetDevice(&dev);
-    if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
-  }
-  if (dev != h->device)
-    return fail(HCGR_ERR_INVALID_ARGUMENT, "stream belongs to device %d, handle to device %d", dev, h->device);
-  int cur = -1;
-  e = hipGetDevice(&cur);
-  if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
-  if (cur != h->device) {
-    e = hipSetDevice(h->device);
-    if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipSetDevice: %s", hipGetErrorString(e));
-  }
-  *prev = cur;
-  return HCGR_OK;
-}
-static void restore_device(hcgr_handle h, int prev) {
-  if (prev != h->device) (void)hipSetDevice(prev);
-}
-
 static hcgr_status forward_impl(hcgr_handle h, const uint16_t* R, const uint16_t* y, const uint16_t* inj,
                                 int64_t ld_inj, const uint16_t* wnorm, const uint16_t* wd, const uint16_t* wi,
                                 const uint16_t* wu, int64_t M, uint16_t* R2, float* rrms, uint16_t* inj_next,
@@ -512,7 +520,7 @@ static hcgr_status forward_impl(hcgr_handle h, const uint16_t* R, const uint16_t
                                  (int)h->table.size());
   if (st != HCGR_OK || M == 0) return st;
   int cur = -1;
-  if ((st = enter_device(h, stream, &cur)) != HCGR_OK) return st;
+  if ((st = enter_device(h->device, stream, &cur)) != HCGR_OK) return st;
   hcgr::ForwardArgs a;
   a.R = R; a.y = y; a.inj = inj; a.wnorm = wnorm; a.wd = wd; a.wi = wi; a.wu = wu;
   a.ld_inj = ld_inj; a.ld_inj_next = ld_inj_next; a.M = M;
@@ -520,7 +528,7 @@ static hcgr_status forward_impl(hcgr_handle h, const uint16_t* R, const uint16_t
   a.res = mix ? R : R2;
   a.wait_polls = h->wait_polls;
   int le = hcgr::launch_forward(h->shape, plan, a, stream, events);
-  restore_device(h, cur);
+  restore_device(h->device, cur);
   if (le != (int)hipSuccess)
     return fail(HCGR_ERR_HIP, "kernel launch failed: %s", hipGetErrorString((hipError_t)le));
   return ok();
@@ -617,11 +625,11 @@ hcgr_status hcgr_combine(hcgr_handle h, const uint16_t* R, const uint16_t* y, co
   hcgr_status st = hcgr_validate_combine(&h->cfg, R, y, inj, ld_inj, M, R2);
   if (st != HCGR_OK || M == 0) return st;
   int cur = -1;
-  if ((st = enter_device(h, stream, &cur)) != HCGR_OK) return st;
+  if ((st = enter_device(h->device, stream, &cur)) != HCGR_OK) return st;
   hcgr::CombineArgs a;
   a.R = R; a.y = y; a.inj = inj; a.ld_inj = ld_inj; a.M = M; a.HS = h->shape.hs; a.HC = h->shape.hc; a.R2 = R2;
   int le = hcgr::launch_combine(a, stream);
-  restore_device(h, cur);
+  restore_device(h->device, cur);
   if (le != (int)hipSuccess)
     return fail(HCGR_ERR_HIP, "kernel launch failed: %s", hipGetErrorString((hipError_t)le));
   return ok();
