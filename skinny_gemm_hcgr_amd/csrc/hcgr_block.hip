@@ -24,40 +24,83 @@ template <> __device__ __forceinline__ uint16_t down<Bf16>(float v) { return to_
 template <> __device__ __forceinline__ _Float16 down<Fp16>(float v) { return (_Float16)v; }
 template <> __device__ __forceinline__ float down<Fp32>(float v) { return v; }
 
-// V values of a row: V = 1, or as many as 16 bytes hold.
-template <typename T, int V>
-__device__ __forceinline__ void load(const typename T::S* p, float (&f)[V]) {
-  if constexpr (V == 1) {
-    f[0] = up(*p);
+// 16 bytes of a row: V = vec<T>() values. n says how many of them the row
+// still has (<= 0: none, they read as zero and are not stored). AL: every row
+// starts on 16 bytes and has a whole number of such pieces; otherwise a piece
+// may start at any element (gfx950 loads and stores 16 bytes at any alignment)
+// and a row's last piece is moved one element at a time.
+template <typename T>
+constexpr int vec() { return 16 / (int)sizeof(typename T::S); }
+
+template <typename T, bool AL>
+__device__ __forceinline__ uint4 load_raw(const typename T::S* p, int n) {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if constexpr (AL) {
+    if (n > 0) u = ld16(p);
   } else {
-    union { uint4 u; typename T::S s[V]; } x;
-    x.u = ld16(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = up(x.s[i]);
+    if (n >= vec<T>()) {
+      __builtin_memcpy(&u, p, 16);
+    } else {
+      typename T::S s[vec<T>()] = {};
+      for (int i = 0; i < vec<T>(); ++i)
+        if (i < n) s[i] = p[i];
+      __builtin_memcpy(&u, s, 16);
+    }
   }
+  return u;
 }
-template <typename T, int V>
-__device__ __forceinline__ void store(typename T::S* p, const float (&f)[V]) {
-  if constexpr (V == 1) {
-    *p = down<T>(f[0]);
-  } else {
-    union { uint4 u; typename T::S s[V]; } x;
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 u, float (&f)[vec<T>()]) {
+  typename T::S s[vec<T>()];
+  __builtin_memcpy(s, &u, 16);
 #pragma unroll
-    for (int i = 0; i < V; ++i) x.s[i] = down<T>(f[i]);
-    st16(p, x.u);
+  for (int i = 0; i < vec<T>(); ++i) f[i] = up(s[i]);
+}
+template <typename T, bool AL>
+__device__ __forceinline__ void load(const typename T::S* p, int n, float (&f)[vec<T>()]) {
+  unpack<T>(load_raw<T, AL>(p, n), f);
+}
+template <typename T, bool AL>
+__device__ __forceinline__ void store(typename T::S* p, int n, const float (&f)[vec<T>()]) {
+  typename T::S s[vec<T>()];
+#pragma unroll
+  for (int i = 0; i < vec<T>(); ++i) s[i] = down<T>(f[i]);
+  if (AL ? n > 0 : n >= vec<T>()) {
+    uint4 u;
+    __builtin_memcpy(&u, s, 16);
+    if constexpr (AL) st16(p, u);
+    else __builtin_memcpy(p, &u, 16);
+  } else if constexpr (!AL) {
+    for (int i = 0; i < vec<T>(); ++i)
+      if (i < n) p[i] = s[i];
   }
 }
 
 // ------------------------------------------------------------ reductions --
+// Over the 64 lanes of a wave, the result in each of them: lanes 1, 2, 4 and 8
+// apart meet through DPP, the rows of 16 through the lane swaps of gfx950.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <typename F>
+__device__ __forceinline__ uint32_t wave_all(uint32_t v, F f) {
+  v = f(v, dpp<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = f(v, dpp<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = f(v, dpp<0x141>(v));  // row_half_mirror
+  v = f(v, dpp<0x140>(v));  // row_mirror
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = f(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return f(b[0], b[1]);
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return __uint_as_float(wave_all(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-  return v;
+  return wave_all(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 // Sum of N values over the workgroup, the same bits in every thread. `red`
 // holds N floats a wave; the caller does not reuse it before a barrier.
@@ -121,18 +164,21 @@ __device__ __forceinline__ int quant1(float v, const Quant& z) {
   const float t = rintf(v * z.pre * z.inv);
   return fabsf(t) <= 127.0f ? (int)t : 0;
 }
-template <int V>
-__device__ __forceinline__ void store_q(int8_t* p, const float (&v)[V], const Quant& z) {
-  if constexpr (V == 1) {
-    *p = (int8_t)quant1(v[0], z);
-  } else {
-    uint32_t w[V / 4];
+// n of V quantized values (rows of q start on 16 bytes and V divides the
+// column, so whole pieces are aligned).
+template <int V, bool AL>
+__device__ __forceinline__ void store_q(int8_t* p, int n, const float (&v)[V], const Quant& z) {
+  uint32_t w[V / 4];
 #pragma unroll
-    for (int i = 0; i < V; i += 4)
-      w[i / 4] = (uint32_t)(quant1(v[i], z) & 255) | (uint32_t)(quant1(v[i + 1], z) & 255) << 8 |
-                 (uint32_t)(quant1(v[i + 2], z) & 255) << 16 | (uint32_t)(quant1(v[i + 3], z) & 255) << 24;
+  for (int i = 0; i < V; i += 4)
+    w[i / 4] = (uint32_t)(quant1(v[i], z) & 255) | (uint32_t)(quant1(v[i + 1], z) & 255) << 8 |
+               (uint32_t)(quant1(v[i + 2], z) & 255) << 16 | (uint32_t)(quant1(v[i + 3], z) & 255) << 24;
+  if (AL ? n > 0 : n >= V) {
     if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
     else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else if constexpr (!AL) {
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
   }
 }
 
@@ -146,9 +192,10 @@ constexpr int kMaxHc = 8;
 // otherwise one stream that is used as it is (hcgr_block_norm, and without
 // NORM the quantizer).
 // ---------------------------------------------------------------------------
-template <typename T, int V, bool RES, bool NORM>
+template <typename T, bool AL, bool RES, bool NORM>
 __global__ __launch_bounds__(1024) void norm_loop(NormArgs a) {
   using S = typename T::S;
+  constexpr int V = vec<T>();
   __shared__ float red[2][16];
   __shared__ uint32_t redq[16];
   const int hs = a.hs, hc = RES ? a.hc : 1, step = (int)blockDim.x * V;
@@ -167,7 +214,7 @@ __global__ __launch_bounds__(1024) void norm_loop(NormArgs a) {
         float ss[1] = {0.0f};
         for (int c = (int)threadIdx.x * V; c < hs; c += step) {
           float f[V];
-          load<T, V>(y + c, f);
+          load<T, AL>(y + c, hs - c, f);
 #pragma unroll
           for (int i = 0; i < V; ++i) ss[0] += f[i] * f[i];
         }
@@ -179,13 +226,13 @@ __global__ __launch_bounds__(1024) void norm_loop(NormArgs a) {
     // u of V channels at c; with WRITE also R2
     auto form = [&](int c, float (&u)[V], bool write) {
       if constexpr (!RES) {
-        load<T, V>(R + c, u);
+        load<T, AL>(R + c, hs - c, u);
       } else {
         float z[V];
-        load<T, V>(y + c, z);
+        load<T, AL>(y + c, hs - c, z);
         if (wpost) {
           float w[V];
-          load<T, V>(wpost + c, w);
+          load<T, AL>(wpost + c, hs - c, w);
 #pragma unroll
           for (int i = 0; i < V; ++i) z[i] = z[i] * ry * (1.0f + w[i]);
         }
@@ -193,13 +240,13 @@ __global__ __launch_bounds__(1024) void norm_loop(NormArgs a) {
         for (int i = 0; i < V; ++i) u[i] = 0.0f;
         for (int s = 0; s < hc; ++s) {
           float r[V];
-          load<T, V>(R + (int64_t)s * hs + c, r);
+          load<T, AL>(R + (int64_t)s * hs + c, hs - c, r);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             r[i] = fmaf(iw[s], z[i], a.rho * r[i]);
             u[i] += r[i];
           }
-          if (write) store<T, V>(R2 + (int64_t)s * hs + c, r);
+          if (write) store<T, AL>(R2 + (int64_t)s * hs + c, hs - c, r);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] /= (float)hc;
@@ -212,7 +259,7 @@ __global__ __launch_bounds__(1024) void norm_loop(NormArgs a) {
       form(c, u, true);
       if (NORM && wpre) {
         float w[V];
-        if (a.q) load<T, V>(wpre + c, w);
+        if (a.q) load<T, AL>(wpre + c, hs - c, w);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           ss[0] += u[i] * u[i];
@@ -243,12 +290,12 @@ __global__ __launch_bounds__(1024) void norm_loop(NormArgs a) {
         form(c, u, false);
         if constexpr (NORM) {
           float w[V];
-          load<T, V>(wpre + c, w);
+          load<T, AL>(wpre + c, hs - c, w);
 #pragma unroll
           for (int i = 0; i < V; ++i) u[i] = u[i] * (1.0f + w[i]) * ru;
-          if (a.x) store<T, V>(reinterpret_cast<S*>(a.x) + m * hs + c, u);
+          if (a.x) store<T, AL>(reinterpret_cast<S*>(a.x) + m * hs + c, hs - c, u);
         }
-        if (a.q) store_q<V>(a.q + m * a.ld_q + c, u, z);
+        if (a.q) store_q<V, AL>(a.q + m * a.ld_q + c, hs - c, u, z);
       }
     }
     __syncthreads();  // the next row reuses the reduction arrays
@@ -276,9 +323,10 @@ constexpr int kColThreads = 256;
 __host__ __device__ inline int64_t bwd_groups(int64_t M) { return M < kRowGroups ? M : kRowGroups; }
 __host__ __device__ inline int64_t bwd_row_floats(int64_t M) { return (2 * M + 3) / 4 * 4; }
 
-template <typename T, int V, bool RES>
+template <typename T, bool AL, bool RES>
 struct BwdRow {
   using S = typename T::S;
+  static constexpr int V = vec<T>();
   const NormBwdArgs& a;
   int64_t m;
   const S *R, *y, *dR2, *dx, *wpost, *wpre;
@@ -299,8 +347,8 @@ struct BwdRow {
   }
   // z = y*ry*(1 + w_post) (h = y*ry, g = 1 + w_post); RES only
   __device__ __forceinline__ void form_z(int c, float (&h)[V], float (&g)[V], float (&z)[V]) const {
-    load<T, V>(y + c, h);
-    if (wpost) load<T, V>(wpost + c, g);
+    load<T, AL>(y + c, a.hs - c, h);
+    if (wpost) load<T, AL>(wpost + c, a.hs - c, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       h[i] *= ry;
@@ -310,13 +358,13 @@ struct BwdRow {
   }
   __device__ __forceinline__ void form_u(int c, const float (&z)[V], float (&u)[V]) const {
     if constexpr (!RES) {
-      load<T, V>(R + c, u);
+      load<T, AL>(R + c, a.hs - c, u);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) u[i] = 0.0f;
       for (int s = 0; s < hc; ++s) {
         float r[V];
-        load<T, V>(R + (int64_t)s * a.hs + c, r);
+        load<T, AL>(R + (int64_t)s * a.hs + c, a.hs - c, r);
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] += fmaf(iw[s], z[i], a.rho * r[i]);
       }
@@ -327,19 +375,20 @@ struct BwdRow {
   // e = dx*(1 + w_pre)
   __device__ __forceinline__ void form_e(int c, float (&d)[V], float (&e)[V]) const {
     float w[V];
-    load<T, V>(dx + c, d);
-    load<T, V>(wpre + c, w);
+    load<T, AL>(dx + c, a.hs - c, d);
+    load<T, AL>(wpre + c, a.hs - c, w);
 #pragma unroll
     for (int i = 0; i < V; ++i) e[i] = d[i] * (1.0f + w[i]);
   }
 };
 
-template <typename T, int V, bool RES>
+template <typename T, bool AL, bool RES>
 __global__ __launch_bounds__(1024) void norm_bwd_rows(NormBwdArgs a) {
+  constexpr int V = vec<T>();
   __shared__ float red[16 * (kMaxHc + 3)];
   float* rows = reinterpret_cast<float*>(a.ws);
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-    const BwdRow<T, V, RES> row(a, m);
+    const BwdRow<T, AL, RES> row(a, m);
     float sums[kMaxHc + 3] = {};  // B_s, A, C, D
     for (int c = (int)threadIdx.x * V; c < a.hs; c += (int)blockDim.x * V) {
       float h[V], g[V], z[V] = {}, u[V], d[V], e[V];
@@ -356,7 +405,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_rows(NormBwdArgs a) {
       }
       if (RES && row.dR2)
         for (int s = 0; s < row.hc; ++s) {
-          load<T, V>(row.dR2 + (int64_t)s * a.hs + c, d);
+          load<T, AL>(row.dR2 + (int64_t)s * a.hs + c, a.hs - c, d);
 #pragma unroll
           for (int i = 0; i < V; ++i) sums[s] += d[i] * z[i];
         }
@@ -381,15 +430,16 @@ __global__ __launch_bounds__(1024) void norm_bwd_rows(NormBwdArgs a) {
   }
 }
 
-template <typename T, int V, bool RES>
+template <typename T, bool AL, bool RES>
 __global__ __launch_bounds__(kColThreads) void norm_bwd_cols(NormBwdArgs a) {
   using S = typename T::S;
+  constexpr int V = vec<T>();
   const int c = ((int)blockIdx.x * kColThreads + (int)threadIdx.x) * V;
   if (c >= a.hs) return;
   const float* rows = reinterpret_cast<const float*>(a.ws);
   float apost[V] = {}, apre[V] = {};
   for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
-    const BwdRow<T, V, RES> row(a, m);
+    const BwdRow<T, AL, RES> row(a, m);
     const float m_pre = rows[2 * m], m_post = rows[2 * m + 1];
     float h[V], g[V], z[V] = {}, u[V], dx[V], e[V], du[V] = {};
     if constexpr (RES) row.form_z(c, h, g, z);
@@ -404,19 +454,19 @@ __global__ __launch_bounds__(kColThreads) void norm_bwd_cols(NormBwdArgs a) {
       }
     }
     if constexpr (!RES) {
-      if (a.dR) store<T, V>(reinterpret_cast<S*>(a.dR) + m * a.hs + c, du);
+      if (a.dR) store<T, AL>(reinterpret_cast<S*>(a.dR) + m * a.hs + c, a.hs - c, du);
     } else {
       float dz[V] = {};
       for (int s = 0; s < row.hc; ++s) {
         float d[V] = {};
-        if (row.dR2) load<T, V>(row.dR2 + (int64_t)s * a.hs + c, d);
+        if (row.dR2) load<T, AL>(row.dR2 + (int64_t)s * a.hs + c, a.hs - c, d);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           d[i] += du[i] / (float)row.hc;
           dz[i] = fmaf(row.iw[s], d[i], dz[i]);
           d[i] *= a.rho;
         }
-        store<T, V>(reinterpret_cast<S*>(a.dR) + m * a.ld_R + (int64_t)s * a.hs + c, d);
+        store<T, AL>(reinterpret_cast<S*>(a.dR) + m * a.ld_R + (int64_t)s * a.hs + c, a.hs - c, d);
       }
       if (row.wpost) {
 #pragma unroll
@@ -425,14 +475,14 @@ __global__ __launch_bounds__(kColThreads) void norm_bwd_cols(NormBwdArgs a) {
           dz[i] = row.ry * (dz[i] * g[i] - h[i] * m_post);
         }
       }
-      store<T, V>(reinterpret_cast<S*>(a.dy) + m * a.hs + c, dz);
+      store<T, AL>(reinterpret_cast<S*>(a.dy) + m * a.hs + c, a.hs - c, dz);
     }
   }
   float* part = reinterpret_cast<float*>(a.ws) + bwd_row_floats(a.M) + (int64_t)blockIdx.y * 2 * a.hs;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (a.dw_post) part[c + i] = apost[i];
-    if (a.dw_pre) part[a.hs + c + i] = apre[i];
+    if (a.dw_post && c + i < a.hs) part[c + i] = apost[i];
+    if (a.dw_pre && c + i < a.hs) part[a.hs + c + i] = apre[i];
   }
 }
 
@@ -451,61 +501,423 @@ __global__ __launch_bounds__(256) void norm_bwd_sum(NormBwdArgs a, int groups) {
   if (w == 0 && c < a.hs) out[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
 }
 
+// ---------------------------------------------------------------------------
+// norm_row: the forward pass of rows that fit the registers of a workgroup
+// (NCH 16-byte pieces of every tensor a thread): each value is read once.
+// Every load of a row is issued before the first reduction. Rows of at most
+// 64 * NCH pieces take one wave, four rows a workgroup, without barriers;
+// wider rows take the whole workgroup.
+// ---------------------------------------------------------------------------
+template <typename T, int HC, int NCH, bool AL, bool RES, bool NORM>
+__global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
+  using S = typename T::S;
+  constexpr int V = vec<T>();
+  __shared__ float red[2][16];
+  __shared__ uint32_t redq[16];
+  const int hs = a.hs;
+  const int64_t m = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y);
+  if (m >= a.M) return;  // blockDim.y > 1 only without barriers
+  const S* R = reinterpret_cast<const S*>(a.R) + m * a.ld_R;
+  const S* wpre = reinterpret_cast<const S*>(a.w_pre);
+  const S* wpost = reinterpret_cast<const S*>(a.w_post);
+  uint4 rr[NCH][HC], yr[NCH], gr[NCH], wr[NCH];
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+    if constexpr (RES) yr[j] = load_raw<T, AL>(reinterpret_cast<const S*>(a.y) + m * a.ld_y + c, hs - c);
+#pragma unroll
+    for (int s = 0; s < HC; ++s) rr[j][s] = load_raw<T, AL>(R + (int64_t)s * hs + c, hs - c);
+    if (RES && wpost) gr[j] = load_raw<T, AL>(wpost + c, hs - c);
+    if (NORM && wpre) wr[j] = load_raw<T, AL>(wpre + c, hs - c);
+  }
+  float u[NCH][V];
+  if constexpr (RES) {
+    float iw[HC];
+#pragma unroll
+    for (int s = 0; s < HC; ++s)
+      iw[s] = a.inj ? gate(up(reinterpret_cast<const S*>(a.inj)[m * a.ld_inj + s]), HC) : 1.0f;
+    float ry = 1.0f;
+    if (wpost) {
+      float ss[1] = {0.0f};
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        float f[V];
+        unpack<T>(yr[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss[0] += f[i] * f[i];
+      }
+      group_sum(ss, red[0]);
+      ry = rrms_of(ss[0], hs, a.eps);
+      if (a.rr_post && threadIdx.x == 0) a.rr_post[m * a.rr_ld] = ry;
+    }
+    S* R2 = reinterpret_cast<S*>(a.R2) + m * a.ld_R;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+      float z[V], w[V];
+      unpack<T>(yr[j], z);
+      if (wpost) {
+        unpack<T>(gr[j], w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = z[i] * ry * (1.0f + w[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[j][i] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < HC; ++s) {
+        float r[V];
+        unpack<T>(rr[j][s], r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          r[i] = fmaf(iw[s], z[i], a.rho * r[i]);
+          u[j][i] += r[i];
+        }
+        store<T, AL>(R2 + (int64_t)s * hs + c, hs - c, r);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) u[j][i] *= 1.0f / (float)HC;
+    }
+    if (!wpre) return;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) unpack<T>(rr[j][0], u[j]);
+  }
+  float ru = 1.0f;
+  if constexpr (NORM) {
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      float w[V];
+      unpack<T>(wr[j], w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        ss[0] += u[j][i] * u[j][i];
+        u[j][i] *= 1.0f + w[i];
+      }
+    }
+    group_sum(ss, red[1]);
+    ru = rrms_of(ss[0], hs, a.eps);
+    if (a.rr_pre && threadIdx.x == 0) a.rr_pre[m * a.rr_ld] = ru;
+  }
+#pragma unroll
+  for (int j = 0; j < NCH; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[j][i] *= ru;
+  if (NORM && a.x) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+      store<T, AL>(reinterpret_cast<S*>(a.x) + m * hs + c, hs - c, u[j]);
+    }
+  }
+  if (a.q) {
+    uint32_t am = 0;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) am = max(am, mag(u[j][i]));
+    const Quant z = quant_of(group_umax(am, redq));
+    if (threadIdx.x == 0) a.q_scale[m] = z.scale;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+      store_q<V, AL>(a.q + m * a.ld_q + c, hs - c, u[j], z);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// norm_bwd_row: the backward pass of rows that fit the registers of a
+// workgroup, in one pass over the data. A workgroup walks every G-th row,
+// keeps the weights and the sums of its columns' weight gradients in
+// registers, and gets all row sums from one reduction (see above norm_bwd_rows).
+// One-wave rows: four rows at a time, the four waves' sums meet in LDS.
+// ---------------------------------------------------------------------------
+template <typename T, int HC, int NCH, bool RES>
+__global__ __launch_bounds__(1024 / NCH) void norm_bwd_row(NormBwdArgs a) {
+  using S = typename T::S;
+  constexpr bool AL = true;
+  constexpr int V = vec<T>(), N = RES ? HC + 3 : 1;
+  __shared__ float red[2][16 * N];
+  __shared__ float wred[3][2][64 * NCH * V];  // one-wave rows only
+  const int hs = a.hs;
+  const S* wpre = reinterpret_cast<const S*>(a.w_pre);
+  const S* wpost = RES ? reinterpret_cast<const S*>(a.w_post) : nullptr;
+  float apost[NCH][V] = {}, apre[NCH][V] = {};
+  uint4 gr[NCH], wr[NCH];
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+    gr[j] = wpost ? load_raw<T, AL>(wpost + c, hs - c) : make_uint4(0, 0, 0, 0);
+    wr[j] = wpre ? load_raw<T, AL>(wpre + c, hs - c) : make_uint4(0, 0, 0, 0);
+  }
+  int flip = 0;
+  const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+  for (int64_t m = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y); m < a.M;
+       m += stride) {
+    const S* R = reinterpret_cast<const S*>(a.R) + m * a.ld_R;
+    uint4 rr[NCH][HC], dr[NCH][HC], yr[NCH], xr[NCH];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+      if constexpr (RES) yr[j] = load_raw<T, AL>(reinterpret_cast<const S*>(a.y) + m * a.ld_y + c, hs - c);
+      if (wpre) {
+        xr[j] = load_raw<T, AL>(reinterpret_cast<const S*>(a.dx) + m * hs + c, hs - c);
+#pragma unroll
+        for (int s = 0; s < HC; ++s) rr[j][s] = load_raw<T, AL>(R + (int64_t)s * hs + c, hs - c);
+      }
+      if constexpr (RES) {
+#pragma unroll
+        for (int s = 0; s < HC; ++s)
+          dr[j][s] = a.dR2 ? load_raw<T, AL>(reinterpret_cast<const S*>(a.dR2) + m * a.ld_R + (int64_t)s * hs + c, hs - c)
+                           : make_uint4(0, 0, 0, 0);
+      }
+    }
+    const float ry = wpost ? a.rr_post[m * a.rr_ld] : 1.0f, ru = wpre ? a.rr_pre[m * a.rr_ld] : 1.0f;
+    float iw[HC], iwm = 0.0f;
+#pragma unroll
+    for (int s = 0; s < HC; ++s) {
+      iw[s] = RES && a.inj ? gate(up(reinterpret_cast<const S*>(a.inj)[m * a.ld_inj + s]), HC) : 1.0f;
+      iwm += iw[s] * (1.0f / (float)HC);
+    }
+    // u, and the row sums B_s, A, C, D
+    float u[NCH][V], sums[N] = {};
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      float z[V], g[V];
+      if constexpr (RES) {
+        unpack<T>(yr[j], z);
+        unpack<T>(gr[j], g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = z[i] * ry * (1.0f + g[i]);
+#pragma unroll
+        for (int s = 0; s < HC; ++s) {
+          float d[V];
+          unpack<T>(dr[j][s], d);
+#pragma unroll
+          for (int i = 0; i < V; ++i) sums[s] += d[i] * z[i];
+        }
+      }
+      if (wpre) {
+        float w[V], e[V];
+        unpack<T>(rr[j][0], u[j]);
+        if constexpr (RES) {
+#pragma unroll
+          for (int s = 1; s < HC; ++s) {
+            float r[V];
+            unpack<T>(rr[j][s], r);
+#pragma unroll
+            for (int i = 0; i < V; ++i) u[j][i] += r[i];
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) u[j][i] = fmaf(iwm, z[i], u[j][i] * (a.rho / (float)HC));
+        }
+        unpack<T>(xr[j], e);
+        unpack<T>(wr[j], w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          e[i] *= 1.0f + w[i];
+          sums[N == 1 ? 0 : HC] += e[i] * u[j][i];
+          if constexpr (RES) {
+            sums[HC + 1] += e[i] * z[i];
+            sums[HC + 2] += u[j][i] * z[i];
+          }
+        }
+      }
+    }
+    group_sum(sums, red[flip]);
+    flip ^= 1;  // the next row's sums go where no thread still reads
+    const float m_pre = wpre ? ru * sums[N == 1 ? 0 : HC] / (float)hs : 0.0f;
+    float m_post = 0.0f;
+    if constexpr (RES) {
+      const float duz = wpre ? ru * (sums[HC + 1] - m_pre * ru * sums[HC + 2]) / (float)HC : 0.0f;
+#pragma unroll
+      for (int s = 0; s < HC; ++s) {
+        const float diw = sums[s] + duz;
+        m_post += iw[s] * diw;
+        if (a.dinj && threadIdx.x == 0)
+          reinterpret_cast<S*>(a.dinj)[m * a.ld_dinj + s] = down<T>(diw * gate_slope(iw[s], HC));
+      }
+      m_post /= (float)hs;
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+      float du[V] = {};
+      if (wpre) {
+        float dx[V], w[V];
+        unpack<T>(xr[j], dx);
+        unpack<T>(wr[j], w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float hu = u[j][i] * ru;
+          du[i] = ru * (dx[i] * (1.0f + w[i]) - hu * m_pre);
+          apre[j][i] += dx[i] * hu;
+        }
+      }
+      if constexpr (!RES) {
+        if (a.dR) store<T, AL>(reinterpret_cast<S*>(a.dR) + m * hs + c, hs - c, du);
+      } else {
+        float dz[V] = {};
+#pragma unroll
+        for (int s = 0; s < HC; ++s) {
+          float d[V];
+          unpack<T>(dr[j][s], d);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            d[i] = fmaf(du[i], 1.0f / (float)HC, d[i]);
+            dz[i] = fmaf(iw[s], d[i], dz[i]);
+            d[i] *= a.rho;
+          }
+          store<T, AL>(reinterpret_cast<S*>(a.dR) + m * a.ld_R + (int64_t)s * hs + c, hs - c, d);
+        }
+        if (wpost) {
+          float h[V], g[V];
+          unpack<T>(yr[j], h);
+          unpack<T>(gr[j], g);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            h[i] *= ry;
+            apost[j][i] += dz[i] * h[i];
+            dz[i] = ry * (dz[i] * (1.0f + g[i]) - h[i] * m_post);
+          }
+        }
+        store<T, AL>(reinterpret_cast<S*>(a.dy) + m * hs + c, hs - c, dz);
+      }
+    }
+  }
+  if (!a.dw_post && !a.dw_pre) return;
+  if (blockDim.y > 1) {  // four waves, blockDim.x = 64
+    const int w = (int)threadIdx.y, t = (int)threadIdx.x;
+    if (w > 0) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          wred[w - 1][0][(j * V + i) * 64 + t] = apost[j][i];
+          wred[w - 1][1][(j * V + i) * 64 + t] = apre[j][i];
+        }
+    }
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          apost[j][i] += wred[k][0][(j * V + i) * 64 + t];
+          apre[j][i] += wred[k][1][(j * V + i) * 64 + t];
+        }
+  }
+  float* part = reinterpret_cast<float*>(a.ws) + bwd_row_floats(a.M) + (int64_t)blockIdx.x * 2 * hs;
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+    if (c >= hs) continue;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      if (a.dw_post)
+        *reinterpret_cast<float4*>(part + c + i) = make_float4(apost[j][i], apost[j][i + 1], apost[j][i + 2], apost[j][i + 3]);
+      if (a.dw_pre)
+        *reinterpret_cast<float4*>(part + hs + c + i) = make_float4(apre[j][i], apre[j][i + 1], apre[j][i + 2], apre[j][i + 3]);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- launches --
 constexpr int64_t kMaxGrid = 1 << 20;
-
-template <typename T>
-constexpr int vec() { return 16 / (int)sizeof(typename T::S); }
 
 bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 bool ld16_ok(int64_t ld, int b) { return ld * b % 16 == 0; }
 
 // Whether every row of the call starts on 16 bytes and HS is whole pieces.
-bool vec_ok(const NormArgs& a, int b) {
+bool aligned(const NormArgs& a, int b) {
   return ld16_ok(a.hs, b) && al16(a.R) && ld16_ok(a.ld_R, b) && al16(a.y) && ld16_ok(a.ld_y, b) && al16(a.w_post) &&
          al16(a.w_pre) && al16(a.R2) && al16(a.x);
 }
-bool vec_ok(const NormBwdArgs& a, int b) {
+bool aligned(const NormBwdArgs& a, int b) {
   return ld16_ok(a.hs, b) && al16(a.R) && ld16_ok(a.ld_R, b) && al16(a.y) && ld16_ok(a.ld_y, b) && al16(a.w_post) &&
          al16(a.w_pre) && al16(a.dR2) && al16(a.dx) && al16(a.dR) && al16(a.dy);
 }
 
-int loop_threads(int hs, int v) {
-  const int64_t t = cdiv64(cdiv64(hs, v), 64) * 64;
+int loop_threads(int64_t pieces) {
+  const int64_t t = cdiv64(pieces, 64) * 64;
   return (int)(t < 1024 ? t : 1024);
 }
 
-template <typename T, int V>
-int norm_forward(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
-  const dim3 grid((unsigned)(a.M < kMaxGrid ? a.M : kMaxGrid)), blk((unsigned)loop_threads(a.hs, V));
-  if (!norm) hipLaunchKernelGGL((norm_loop<T, V, false, false>), grid, blk, 0, st, a);
-  else if (residual) hipLaunchKernelGGL((norm_loop<T, V, true, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((norm_loop<T, V, false, true>), grid, blk, 0, st, a);
+template <typename T, bool AL>
+int forward_loop(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
+  const dim3 grid((unsigned)(a.M < kMaxGrid ? a.M : kMaxGrid)), blk((unsigned)loop_threads(cdiv64(a.hs, vec<T>())));
+  if (!norm) hipLaunchKernelGGL((norm_loop<T, AL, false, false>), grid, blk, 0, st, a);
+  else if (residual) hipLaunchKernelGGL((norm_loop<T, AL, true, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((norm_loop<T, AL, false, true>), grid, blk, 0, st, a);
   return (int)hipGetLastError();
 }
 
-template <typename T, int V, bool RES>
-int norm_backward(const NormBwdArgs& a, hipStream_t st) {
-  const int64_t groups = bwd_groups(a.M);
-  hipLaunchKernelGGL((norm_bwd_rows<T, V, RES>), dim3((unsigned)(a.M < kMaxGrid ? a.M : kMaxGrid)),
-                     dim3((unsigned)loop_threads(a.hs, V)), 0, st, a);
-  hipLaunchKernelGGL((norm_bwd_cols<T, V, RES>),
-                     dim3((unsigned)cdiv64(a.hs, kColThreads * V), (unsigned)groups), dim3(kColThreads), 0, st, a);
-  if (a.dw_post || a.dw_pre)
-    hipLaunchKernelGGL(norm_bwd_sum, dim3((unsigned)cdiv64(a.hs, 64), 2), dim3(256), 0, st, a, (int)groups);
+template <typename T, int NCH, bool AL>
+int forward_row(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
+  const int64_t pieces = cdiv64(a.hs, vec<T>());
+  const int nw = (int)cdiv64(pieces, 64 * NCH);
+  const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1), grid((unsigned)cdiv64(a.M, blk.y));
+  if (!norm) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, false>), grid, blk, 0, st, a);
+  else if (!residual) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, true>), grid, blk, 0, st, a);
+  else if (a.hc == 1) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, true, true>), grid, blk, 0, st, a);
+  else if (a.hc == 2) hipLaunchKernelGGL((norm_row<T, 2, NCH, AL, true, true>), grid, blk, 0, st, a);
+  else if (a.hc == 4) hipLaunchKernelGGL((norm_row<T, 4, NCH, AL, true, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((norm_row<T, 8, NCH, AL, true, true>), grid, blk, 0, st, a);
   return (int)hipGetLastError();
 }
 
 template <typename T>
 int forward_of(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
-  return vec_ok(a, (int)sizeof(typename T::S)) ? norm_forward<T, vec<T>()>(a, residual, norm, st)
-                                               : norm_forward<T, 1>(a, residual, norm, st);
+  const bool al = aligned(a, (int)sizeof(typename T::S));
+  const int64_t pieces = cdiv64(a.hs, vec<T>());
+  if (a.M >= (int64_t)1 << 31) return forward_loop<T, false>(a, residual, norm, st);  // past the largest grid
+  if (!al) return forward_loop<T, false>(a, residual, norm, st);
+  if (pieces <= 1024) return forward_row<T, 1, true>(a, residual, norm, st);
+  if (pieces <= 2048) return forward_row<T, 2, true>(a, residual, norm, st);
+  return forward_loop<T, true>(a, residual, norm, st);
 }
+
+int sum_groups(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
+  if (a.dw_post || a.dw_pre)
+    hipLaunchKernelGGL(norm_bwd_sum, dim3((unsigned)cdiv64(a.hs, 64), 2), dim3(256), 0, st, a, (int)groups);
+  return (int)hipGetLastError();
+}
+
+template <typename T, bool AL, bool RES>
+int backward_loop(const NormBwdArgs& a, hipStream_t st) {
+  const int64_t groups = bwd_groups(a.M), pieces = cdiv64(a.hs, vec<T>());
+  hipLaunchKernelGGL((norm_bwd_rows<T, AL, RES>), dim3((unsigned)(a.M < kMaxGrid ? a.M : kMaxGrid)),
+                     dim3((unsigned)loop_threads(pieces)), 0, st, a);
+  hipLaunchKernelGGL((norm_bwd_cols<T, AL, RES>), dim3((unsigned)cdiv64(pieces, kColThreads), (unsigned)groups),
+                     dim3(kColThreads), 0, st, a);
+  return sum_groups(a, groups, st);
+}
+
+template <typename T, int NCH>
+int backward_row(const NormBwdArgs& a, bool residual, hipStream_t st) {
+  const int64_t pieces = cdiv64(a.hs, vec<T>());
+  const int nw = (int)cdiv64(pieces, 64 * NCH);
+  const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1);
+  const int64_t groups = bwd_groups(cdiv64(a.M, blk.y));
+  const dim3 grid((unsigned)groups);
+  if (!residual) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, false>), grid, blk, 0, st, a);
+  else if (a.hc == 1) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, true>), grid, blk, 0, st, a);
+  else if (a.hc == 2) hipLaunchKernelGGL((norm_bwd_row<T, 2, NCH, true>), grid, blk, 0, st, a);
+  else if (a.hc == 4) hipLaunchKernelGGL((norm_bwd_row<T, 4, NCH, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((norm_bwd_row<T, 8, NCH, true>), grid, blk, 0, st, a);
+  return sum_groups(a, groups, st);
+}
+
 template <typename T>
 int backward_of(const NormBwdArgs& a, bool residual, hipStream_t st) {
-  if (vec_ok(a, (int)sizeof(typename T::S)))
-    return residual ? norm_backward<T, vec<T>(), true>(a, st) : norm_backward<T, vec<T>(), false>(a, st);
-  return residual ? norm_backward<T, 1, true>(a, st) : norm_backward<T, 1, false>(a, st);
+  const int64_t pieces = cdiv64(a.hs, vec<T>());
+  if (!aligned(a, (int)sizeof(typename T::S)))
+    return residual ? backward_loop<T, false, true>(a, st) : backward_loop<T, false, false>(a, st);
+  if (pieces <= 1024) return backward_row<T, 1>(a, residual, st);
+  return residual ? backward_loop<T, true, true>(a, st) : backward_loop<T, true, false>(a, st);
 }
 
 int dispatch(const NormArgs& a, int dtype, bool residual, bool norm, void* stream) {
