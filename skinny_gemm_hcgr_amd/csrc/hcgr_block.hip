@@ -486,19 +486,52 @@ __global__ __launch_bounds__(kColThreads) void norm_bwd_cols(NormBwdArgs a) {
   }
 }
 
-__global__ __launch_bounds__(256) void norm_bwd_sum(NormBwdArgs a, int groups) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x % 64, w = threadIdx.x / 64;
-  const int c = (int)blockIdx.x * 64 + lane;
+__global__ __launch_bounds__(1024) void norm_bwd_sum(NormBwdArgs a, int groups) {
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  const int c = (int)blockIdx.x * 32 + lane;
   float* out = blockIdx.y ? a.dw_pre : a.dw_post;
   if (!out) return;
   const float* part = reinterpret_cast<const float*>(a.ws) + bwd_row_floats(a.M) + (int64_t)blockIdx.y * a.hs;
   float s = 0.0f;
-  if (c < a.hs)
-    for (int g = w; g < groups; g += 4) s += part[(int64_t)g * 2 * a.hs + c];
+  if (c < a.hs) {
+#pragma unroll 8
+    for (int g = w; g < groups; g += 32) s += part[(int64_t)g * 2 * a.hs + c];
+  }
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < a.hs) out[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  s = red[lane][w];  // wave w/2 holds column w of the 32 partial sums in lanes (w % 2)*32 ..
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if (lane == 0 && (int)blockIdx.x * 32 + w < a.hs) out[(int)blockIdx.x * 32 + w] = s;
+}
+
+// Rows as buffer ranges: one 32-bit offset a piece serves every tensor and
+// stream (the stream's offset is scalar), a piece past the row reads as zero
+// and is not stored, and so does every piece of an absent tensor.
+template <typename S>
+__device__ __forceinline__ rsrc_t row_of(const void* base, int64_t off, uint32_t bytes) {
+  return base ? make_rsrc(reinterpret_cast<const S*>(base) + off, bytes) : make_rsrc(nullptr, 0u);
+}
+__device__ __forceinline__ uint32_t piece_at(int j, uint32_t row) {
+  const uint32_t at = (threadIdx.x + (uint32_t)j * blockDim.x) * 16u;
+  return at < row ? at : 0x7ffffff0u;
+}
+__device__ __forceinline__ uint4 piece(rsrc_t r, uint32_t at, uint32_t stream = 0) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, (int)stream, 0));
+}
+// The stream's offset goes into the vector offset here: after a 16-byte buffer
+// store whose scalar offset is a register, the compiler lets the next
+// instruction overwrite the stored registers, and on MI355X such stores have
+// written the new values (with a constant scalar offset it keeps them apart).
+template <typename T>
+__device__ __forceinline__ void put(rsrc_t r, uint32_t at, uint32_t stream, const float (&f)[vec<T>()]) {
+  typename T::S s[vec<T>()];
+#pragma unroll
+  for (int i = 0; i < vec<T>(); ++i) s[i] = down<T>(f[i]);
+  u32x4_t u;
+  __builtin_memcpy(&u, s, 16);
+  __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)(at + stream), 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -508,7 +541,7 @@ __global__ __launch_bounds__(256) void norm_bwd_sum(NormBwdArgs a, int groups) {
 // 64 * NCH pieces take one wave, four rows a workgroup, without barriers;
 // wider rows take the whole workgroup.
 // ---------------------------------------------------------------------------
-template <typename T, int HC, int NCH, bool AL, bool RES, bool NORM>
+template <typename T, int HC, int NCH, bool RES, bool NORM>
 __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
   using S = typename T::S;
   constexpr int V = vec<T>();
@@ -517,18 +550,19 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
   const int hs = a.hs;
   const int64_t m = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y);
   if (m >= a.M) return;  // blockDim.y > 1 only without barriers
-  const S* R = reinterpret_cast<const S*>(a.R) + m * a.ld_R;
-  const S* wpre = reinterpret_cast<const S*>(a.w_pre);
-  const S* wpost = reinterpret_cast<const S*>(a.w_post);
+  const bool wpre = a.w_pre != nullptr, wpost = RES && a.w_post != nullptr;
+  const uint32_t row = (uint32_t)hs * sizeof(S);  // bytes of a stream
+  const rsrc_t rR = row_of<S>(a.R, m * a.ld_R, HC * row), rY = row_of<S>(a.y, m * a.ld_y, row);
+  const rsrc_t rG = row_of<S>(a.w_post, 0, row), rW = row_of<S>(a.w_pre, 0, row);
   uint4 rr[NCH][HC], yr[NCH], gr[NCH], wr[NCH];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-    if constexpr (RES) yr[j] = load_raw<T, AL>(reinterpret_cast<const S*>(a.y) + m * a.ld_y + c, hs - c);
+    const uint32_t at = piece_at(j, row);
+    if constexpr (RES) yr[j] = piece(rY, at);
 #pragma unroll
-    for (int s = 0; s < HC; ++s) rr[j][s] = load_raw<T, AL>(R + (int64_t)s * hs + c, hs - c);
-    if (RES && wpost) gr[j] = load_raw<T, AL>(wpost + c, hs - c);
-    if (NORM && wpre) wr[j] = load_raw<T, AL>(wpre + c, hs - c);
+    for (int s = 0; s < HC; ++s) rr[j][s] = piece(rR, at, s * row);
+    if (wpost) gr[j] = piece(rG, at);
+    if (NORM && wpre) wr[j] = piece(rW, at);
   }
   float u[NCH][V];
   if constexpr (RES) {
@@ -550,10 +584,10 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
       ry = rrms_of(ss[0], hs, a.eps);
       if (a.rr_post && threadIdx.x == 0) a.rr_post[m * a.rr_ld] = ry;
     }
-    S* R2 = reinterpret_cast<S*>(a.R2) + m * a.ld_R;
+    const rsrc_t r2 = row_of<S>(a.R2, m * a.ld_R, HC * row);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+      const uint32_t at = piece_at(j, row);
       float z[V], w[V];
       unpack<T>(yr[j], z);
       if (wpost) {
@@ -572,7 +606,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
           r[i] = fmaf(iw[s], z[i], a.rho * r[i]);
           u[j][i] += r[i];
         }
-        store<T, AL>(R2 + (int64_t)s * hs + c, hs - c, r);
+        put<T>(r2, at, s * row, r);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) u[j][i] *= 1.0f / (float)HC;
@@ -605,10 +639,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
     for (int i = 0; i < V; ++i) u[j][i] *= ru;
   if (NORM && a.x) {
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-      store<T, AL>(reinterpret_cast<S*>(a.x) + m * hs + c, hs - c, u[j]);
-    }
+    for (int j = 0; j < NCH; ++j) put<T>(row_of<S>(a.x, m * hs, row), piece_at(j, row), 0, u[j]);
   }
   if (a.q) {
     uint32_t am = 0;
@@ -621,7 +652,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-      store_q<V, AL>(a.q + m * a.ld_q + c, hs - c, u[j], z);
+      store_q<V, true>(a.q + m * a.ld_q + c, hs - c, u[j], z);
     }
   }
 }
@@ -633,44 +664,42 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
 // registers, and gets all row sums from one reduction (see above norm_bwd_rows).
 // One-wave rows: four rows at a time, the four waves' sums meet in LDS.
 // ---------------------------------------------------------------------------
-template <typename T, int HC, int NCH, bool RES>
-__global__ __launch_bounds__(1024 / NCH) void norm_bwd_row(NormBwdArgs a) {
+template <typename T, int HC, int NCH, int THREADS, bool RES>
+__global__ __launch_bounds__(THREADS) void norm_bwd_row(NormBwdArgs a) {
   using S = typename T::S;
-  constexpr bool AL = true;
   constexpr int V = vec<T>(), N = RES ? HC + 3 : 1;
   __shared__ float red[2][16 * N];
   __shared__ float wred[3][2][64 * NCH * V];  // one-wave rows only
   const int hs = a.hs;
-  const S* wpre = reinterpret_cast<const S*>(a.w_pre);
-  const S* wpost = RES ? reinterpret_cast<const S*>(a.w_post) : nullptr;
+  const bool wpre = a.w_pre != nullptr, wpost = RES && a.w_post != nullptr;
+  const uint32_t row = (uint32_t)hs * sizeof(S);  // bytes of a stream
   float apost[NCH][V] = {}, apre[NCH][V] = {};
   uint4 gr[NCH], wr[NCH];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-    gr[j] = wpost ? load_raw<T, AL>(wpost + c, hs - c) : make_uint4(0, 0, 0, 0);
-    wr[j] = wpre ? load_raw<T, AL>(wpre + c, hs - c) : make_uint4(0, 0, 0, 0);
+    gr[j] = piece(row_of<S>(a.w_post, 0, row), piece_at(j, row));
+    wr[j] = piece(row_of<S>(a.w_pre, 0, row), piece_at(j, row));
   }
   int flip = 0;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
   for (int64_t m = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y); m < a.M;
        m += stride) {
-    const S* R = reinterpret_cast<const S*>(a.R) + m * a.ld_R;
+    // an absent tensor is an empty range, which reads as zero
+    const rsrc_t rR = row_of<S>(a.R, m * a.ld_R, HC * row), rD = row_of<S>(a.dR2, m * a.ld_R, HC * row);
+    const rsrc_t rY = row_of<S>(a.y, m * a.ld_y, row), rX = row_of<S>(a.dx, m * hs, row);
     uint4 rr[NCH][HC], dr[NCH][HC], yr[NCH], xr[NCH];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-      if constexpr (RES) yr[j] = load_raw<T, AL>(reinterpret_cast<const S*>(a.y) + m * a.ld_y + c, hs - c);
+      const uint32_t at = piece_at(j, row);
+      if constexpr (RES) yr[j] = piece(rY, at);
       if (wpre) {
-        xr[j] = load_raw<T, AL>(reinterpret_cast<const S*>(a.dx) + m * hs + c, hs - c);
+        xr[j] = piece(rX, at);
 #pragma unroll
-        for (int s = 0; s < HC; ++s) rr[j][s] = load_raw<T, AL>(R + (int64_t)s * hs + c, hs - c);
+        for (int s = 0; s < HC; ++s) rr[j][s] = piece(rR, at, s * row);
       }
       if constexpr (RES) {
 #pragma unroll
-        for (int s = 0; s < HC; ++s)
-          dr[j][s] = a.dR2 ? load_raw<T, AL>(reinterpret_cast<const S*>(a.dR2) + m * a.ld_R + (int64_t)s * hs + c, hs - c)
-                           : make_uint4(0, 0, 0, 0);
+        for (int s = 0; s < HC; ++s) dr[j][s] = piece(rD, at, s * row);
       }
     }
     const float ry = wpost ? a.rr_post[m * a.rr_ld] : 1.0f, ru = wpre ? a.rr_pre[m * a.rr_ld] : 1.0f;
@@ -742,7 +771,7 @@ __global__ __launch_bounds__(1024 / NCH) void norm_bwd_row(NormBwdArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
+      const uint32_t at = piece_at(j, row);
       float du[V] = {};
       if (wpre) {
         float dx[V], w[V];
@@ -756,7 +785,7 @@ __global__ __launch_bounds__(1024 / NCH) void norm_bwd_row(NormBwdArgs a) {
         }
       }
       if constexpr (!RES) {
-        if (a.dR) store<T, AL>(reinterpret_cast<S*>(a.dR) + m * hs + c, hs - c, du);
+        if (a.dR) put<T>(row_of<S>(a.dR, m * hs, row), at, 0, du);
       } else {
         float dz[V] = {};
 #pragma unroll
@@ -769,7 +798,7 @@ __global__ __launch_bounds__(1024 / NCH) void norm_bwd_row(NormBwdArgs a) {
             dz[i] = fmaf(iw[s], d[i], dz[i]);
             d[i] *= a.rho;
           }
-          store<T, AL>(reinterpret_cast<S*>(a.dR) + m * a.ld_R + (int64_t)s * hs + c, hs - c, d);
+          put<T>(row_of<S>(a.dR, m * a.ld_R, HC * row), at, s * row, d);
         }
         if (wpost) {
           float h[V], g[V];
@@ -782,7 +811,7 @@ __global__ __launch_bounds__(1024 / NCH) void norm_bwd_row(NormBwdArgs a) {
             dz[i] = ry * (dz[i] * (1.0f + g[i]) - h[i] * m_post);
           }
         }
-        store<T, AL>(reinterpret_cast<S*>(a.dy) + m * hs + c, hs - c, dz);
+        put<T>(row_of<S>(a.dy, m * hs, row), at, 0, dz);
       }
     }
   }
@@ -855,17 +884,17 @@ int forward_loop(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
   return (int)hipGetLastError();
 }
 
-template <typename T, int NCH, bool AL>
+template <typename T, int NCH>
 int forward_row(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   const int nw = (int)cdiv64(pieces, 64 * NCH);
   const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1), grid((unsigned)cdiv64(a.M, blk.y));
-  if (!norm) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, false>), grid, blk, 0, st, a);
-  else if (!residual) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, true>), grid, blk, 0, st, a);
-  else if (a.hc == 1) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, true, true>), grid, blk, 0, st, a);
-  else if (a.hc == 2) hipLaunchKernelGGL((norm_row<T, 2, NCH, AL, true, true>), grid, blk, 0, st, a);
-  else if (a.hc == 4) hipLaunchKernelGGL((norm_row<T, 4, NCH, AL, true, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((norm_row<T, 8, NCH, AL, true, true>), grid, blk, 0, st, a);
+  if (!norm) hipLaunchKernelGGL((norm_row<T, 1, NCH, false, false>), grid, blk, 0, st, a);
+  else if (!residual) hipLaunchKernelGGL((norm_row<T, 1, NCH, false, true>), grid, blk, 0, st, a);
+  else if (a.hc == 1) hipLaunchKernelGGL((norm_row<T, 1, NCH, true, true>), grid, blk, 0, st, a);
+  else if (a.hc == 2) hipLaunchKernelGGL((norm_row<T, 2, NCH, true, true>), grid, blk, 0, st, a);
+  else if (a.hc == 4) hipLaunchKernelGGL((norm_row<T, 4, NCH, true, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((norm_row<T, 8, NCH, true, true>), grid, blk, 0, st, a);
   return (int)hipGetLastError();
 }
 
@@ -875,14 +904,14 @@ int forward_of(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   if (a.M >= (int64_t)1 << 31) return forward_loop<T, false>(a, residual, norm, st);  // past the largest grid
   if (!al) return forward_loop<T, false>(a, residual, norm, st);
-  if (pieces <= 1024) return forward_row<T, 1, true>(a, residual, norm, st);
-  if (pieces <= 2048) return forward_row<T, 2, true>(a, residual, norm, st);
+  if (pieces <= 1024) return forward_row<T, 1>(a, residual, norm, st);
+  if (pieces <= 2048) return forward_row<T, 2>(a, residual, norm, st);
   return forward_loop<T, true>(a, residual, norm, st);
 }
 
 int sum_groups(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
   if (a.dw_post || a.dw_pre)
-    hipLaunchKernelGGL(norm_bwd_sum, dim3((unsigned)cdiv64(a.hs, 64), 2), dim3(256), 0, st, a, (int)groups);
+    hipLaunchKernelGGL(norm_bwd_sum, dim3((unsigned)cdiv64(a.hs, 32), 2), dim3(1024), 0, st, a, (int)groups);
   return (int)hipGetLastError();
 }
 
@@ -896,18 +925,18 @@ int backward_loop(const NormBwdArgs& a, hipStream_t st) {
   return sum_groups(a, groups, st);
 }
 
-template <typename T, int NCH>
+template <typename T, int NCH, int THREADS>
 int backward_row(const NormBwdArgs& a, bool residual, hipStream_t st) {
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   const int nw = (int)cdiv64(pieces, 64 * NCH);
   const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1);
   const int64_t groups = bwd_groups(cdiv64(a.M, blk.y));
   const dim3 grid((unsigned)groups);
-  if (!residual) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, false>), grid, blk, 0, st, a);
-  else if (a.hc == 1) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, true>), grid, blk, 0, st, a);
-  else if (a.hc == 2) hipLaunchKernelGGL((norm_bwd_row<T, 2, NCH, true>), grid, blk, 0, st, a);
-  else if (a.hc == 4) hipLaunchKernelGGL((norm_bwd_row<T, 4, NCH, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((norm_bwd_row<T, 8, NCH, true>), grid, blk, 0, st, a);
+  if (!residual) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, false>), grid, blk, 0, st, a);
+  else if (a.hc == 1) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, true>), grid, blk, 0, st, a);
+  else if (a.hc == 2) hipLaunchKernelGGL((norm_bwd_row<T, 2, NCH, THREADS, true>), grid, blk, 0, st, a);
+  else if (a.hc == 4) hipLaunchKernelGGL((norm_bwd_row<T, 4, NCH, THREADS, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((norm_bwd_row<T, 8, NCH, THREADS, true>), grid, blk, 0, st, a);
   return sum_groups(a, groups, st);
 }
 
@@ -916,7 +945,10 @@ int backward_of(const NormBwdArgs& a, bool residual, hipStream_t st) {
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   if (!aligned(a, (int)sizeof(typename T::S)))
     return residual ? backward_loop<T, false, true>(a, st) : backward_loop<T, false, false>(a, st);
-  if (pieces <= 1024) return backward_row<T, 1>(a, residual, st);
+  // up to 512 threads a thread has 256 registers, which eight streams need;
+  // above, 128 (some rows then pass through scratch memory)
+  if (pieces <= 512) return backward_row<T, 1, 512>(a, residual, st);
+  if (pieces <= 1024) return backward_row<T, 1, 1024>(a, residual, st);
   return residual ? backward_loop<T, true, true>(a, st) : backward_loop<T, true, false>(a, st);
 }
 
