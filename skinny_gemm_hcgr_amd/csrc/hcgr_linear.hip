@@ -1,9 +1,11 @@
 // hcgr_linear.hip -- the 8-bit linear layer (hcgr_linear_forward):
 //   out[m, n] = (sum_k q[m, k]*w[n, k]) * q_scale[m] * w_scale[n] + bias[n]
-// on v_mfma_i32_16x16x64_i8. Weight rows are the first (row) operand and
+// on MFMA. Weight rows are the first (row) operand and
 // tokens the second (column) operand, so a lane ends with four neighbouring
 // output channels of one token.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "hcgr_block.h"
 #include "hcgr_device.h"
@@ -24,6 +26,10 @@ __device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
   return make_uint4(word(v.x, n), word(v.y, n - 4), word(v.z, n - 8), word(v.w, n - 12));
 }
 
+// An offset past every range (at most 256 rows of 2^22 bytes), also with a
+// row's bytes added.
+constexpr uint32_t kOut = 0x7ffffff0u;
+
 // Output element types: 0 bf16, 1 fp16, 2 fp32.
 template <int DT>
 __device__ __forceinline__ float bias_at(const void* bias, int n) {
@@ -38,60 +44,324 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v) {
   else reinterpret_cast<float*>(out)[i] = v;
 }
 
-// ---------------------------------------------------------------------------
-// linear_direct: a workgroup of four waves owns 64 output channels (16 a
-// wave) of 64 tokens; operands go straight from memory into MFMA registers.
-// ---------------------------------------------------------------------------
+// Four output channels n .. n+3 of token m from their sums. VEC: the row's
+// pieces of four values are aligned and whole.
+template <int DT, bool VEC>
+__device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int n, float qs, const float (&ws)[4],
+                                       const float (&bias)[4], const int (&acc)[4]) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = fmaf((float)acc[i], qs * ws[i], bias[i]);
+  const int64_t at = m * a.ld_out + n;
+  if constexpr (VEC) {
+    if constexpr (DT == 0) {
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+          make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+    } else if constexpr (DT == 1) {
+      typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<f16x4_t*>(reinterpret_cast<_Float16*>(a.out) + at) =
+          f16x4_t{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    } else {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.n) store1<DT>(a.out, at + i, v[i]);
+  }
+}
+// Scales and bias of channels n .. n+3 (zero past N).
 template <int DT>
-__global__ __launch_bounds__(256) void linear_direct(LinearArgs a) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+__device__ __forceinline__ void channel4(const LinearArgs& a, int n, float (&ws)[4], float (&bias)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool in = n + i < a.n;
+    ws[i] = in ? a.w_scale[n + i] : 0.0f;
+    bias[i] = in && a.bias ? bias_at<DT>(a.bias, n + i) : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// linear_skinny: up to 16*MT tokens. The product streams the weights once, so
+// it is bound by their bytes: a workgroup owns `rows` (1..16) output channels,
+// its waves share K in units of 128 bytes (a wave's loads cover whole lines of
+// its rows), and the operands go straight from memory into MFMA registers,
+// U units of weights ahead. The waves' sums meet in LDS.
+// ---------------------------------------------------------------------------
+template <int DT, int MT, int U>
+__global__ __launch_bounds__(1024) void linear_skinny(LinearArgs a, int rows) {
+  extern __shared__ int32_t part[];  // [waves][MT][64 lanes][4]
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, nw = (int)blockDim.x / 64;
   const int r16 = lane % 16, kq = lane / 16;
-  const int n0 = (int)blockIdx.x * 64 + wave * 16;
-  const int64_t m0 = (int64_t)blockIdx.y * 64;
-  if (n0 >= a.n) return;
-  const int k16 = (a.k + 15) / 16 * 16;
-  const int nr = min(16, a.n - n0), mr = (int)min((int64_t)64, a.M - m0);
-  // ranges over the tile's own rows: rows past the last are never in range
+  const int n0 = (int)blockIdx.x * rows;
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int k16 = (a.k + 15) / 16 * 16, units = (a.k + 127) / 128;
+  const int nr = min(rows, a.n - n0), mr = (int)min((int64_t)(16 * MT), a.M - m0);
   const rsrc_t rw = make_rsrc(a.w + (int64_t)n0 * a.ld_w, (uint32_t)((nr - 1) * a.ld_w + k16));
   const rsrc_t rq = make_rsrc(a.q + m0 * a.ld_q, (uint32_t)((mr - 1) * a.ld_q + k16));
-  constexpr uint32_t kOut = 0x7ffffff0u;  // past every range (at most 64 rows of 2^22 bytes)
-  i32x4_t acc[4] = {};
-  for (int k0 = 0; k0 < a.k; k0 += 64) {
-    const int k = k0 + kq * 16;
-    const uint4 w = bld16(rw, k < a.k && r16 < nr ? (uint32_t)(r16 * a.ld_w) + (uint32_t)k : kOut);
+  // rows past the last and bytes past the row's last piece read as zero
+  const uint32_t wrow = r16 < nr ? (uint32_t)(r16 * a.ld_w) : kOut;
+  uint32_t qrow[MT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r = t * 16 + r16;
-      uint4 x = bld16(rq, k < a.k && r < mr ? (uint32_t)(r * a.ld_q) + (uint32_t)k : kOut);
-      x = keep_bytes(x, a.k - k);  // a row's bytes past K count as zero
-      acc[t] = mfma_i8(w, x, acc[t]);
+  for (int t = 0; t < MT; ++t) qrow[t] = t * 16 + r16 < mr ? (uint32_t)((t * 16 + r16) * a.ld_q) : kOut;
+  i32x4_t acc[MT] = {};
+  for (int u0 = wave; u0 < units; u0 += nw * U) {
+    uint4 w[U][2], x[2][MT][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = (u0 + i * nw) * 128 + kq * 32;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[i][h] = bld16_nt(rw, k + 16 * h < k16 ? wrow + (uint32_t)(k + 16 * h) : kOut);
+    }
+    auto load_x = [&](int i) {  // tokens: one unit ahead, they come from the caches
+      const int k = (u0 + i * nw) * 128 + kq * 32;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          x[i % 2][t][h] = bld16(rq, k + 16 * h < k16 ? qrow[t] + (uint32_t)(k + 16 * h) : kOut);
+    };
+    load_x(0);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = (u0 + i * nw) * 128 + kq * 32;
+      if (i + 1 < U) load_x(i + 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (a.k % 16 && k + 16 * h + 16 > a.k) w[i][h] = keep_bytes(w[i][h], a.k - k - 16 * h);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = mfma_i8(w[i][h], x[i % 2][t][h], acc[t]);
+      }
     }
   }
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int64_t m = m0 + t * 16 + r16;
-    if (m >= a.M) continue;
-    const float qs = a.q_scale[m];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + kq * 4 + i;
-      if (n >= a.n) continue;
-      float v = (float)acc[t][i] * (qs * a.w_scale[n]);
-      if (a.bias) v += bias_at<DT>(a.bias, n);
-      store1<DT>(a.out, m * a.ld_out + n, v);
-    }
+  for (int t = 0; t < MT; ++t)
+    *reinterpret_cast<i32x4_t*>(part + ((wave * MT + t) * 64 + lane) * 4) = acc[t];
+  __syncthreads();
+  // thread -> (token, channel); the sums of channel c of token t*16 + r are
+  // word c % 4 of lane (c/4)*16 + r
+  for (int i = threadIdx.x; i < 256 * MT; i += blockDim.x) {
+    const int c = i % 16, r = i / 16 % 16, t = i / 256;
+    if (c >= nr || t * 16 + r >= mr) continue;
+    int sum = 0;
+    for (int v = 0; v < nw; ++v) sum += part[((v * MT + t) * 64 + (c / 4) * 16 + r) * 4 + c % 4];
+    const int64_t m = m0 + t * 16 + r;
+    const int n = n0 + c;
+    const float b = a.bias ? bias_at<DT>(a.bias, n) : 0.0f;
+    store1<DT>(a.out, m * a.ld_out + n, fmaf((float)sum, a.q_scale[m] * a.w_scale[n], b));
   }
+}
+
+// ---------------------------------------------------------------------------
+// linear_tile: TM tokens x TN channels a workgroup, 4 waves as 2 x 2, each
+// (TM/2) x (TN/2) on v_mfma_i32_32x32x32_i8. K passes through LDS in stages of
+// 128 bytes a row, two buffers, written by direct loads: 1 KB an instruction,
+// 8 rows of 8 pieces, piece p of row r holding the row's piece p ^ (r % 8), so
+// that eight lanes reading one piece of eight rows meet every bank once. Half
+// a stage's fragments are read while the other half's products run; the one
+// barrier of a stage stands between its last read and the loads that reuse
+// its buffer, which have a whole stage's products to arrive in.
+// ---------------------------------------------------------------------------
+typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
+
+template <int N>
+using ic = std::integral_constant<int, N>;
+
+template <int TM, int TN>
+constexpr int stage_bytes() { return (TM + TN) * 128; }
+
+// The four words of make_rsrc's descriptor.
+__device__ __forceinline__ i32x4_t range_words(const void* base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)p), __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xffff),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// 1 KB from memory to LDS at `lds` (lane l's 16 bytes at lds + 16*l). Written
+// as assembly so that the compiler does not make every LDS read wait for all
+// loads in flight: the kernel waits itself (stage_landed). It writes no
+// registers but m0.
+__device__ __forceinline__ void load_lds(i32x4_t r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(r), "s"(lds)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void stage_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <int DT, int TM, int TN, bool VEC>
+__global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile(LinearArgs a, int tiles_m, int tiles_n) {
+  extern __shared__ uint8_t lds[];
+  constexpr int FM = TM / 64, FN = TN / 64, SB = stage_bytes<TM, TN>();
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+  const int wm = wave % 2, wn = wave / 2;
+  // Tiles in order: workgroups b, b + 8, b + 16, .. share an XCD and take
+  // neighbouring tiles, eight rows of tiles at a time, so that they meet in
+  // that XCD's L2.
+  const int tiles = tiles_m * tiles_n, per = (tiles + 7) / 8;
+  const int tile = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if ((int)(blockIdx.x / 8) >= per || tile >= tiles) return;  // the whole workgroup
+  const int band = tile / (8 * tiles_n), in = tile % (8 * tiles_n), high = min(8, tiles_m - band * 8);
+  const int64_t m0 = (int64_t)(band * 8 + in % high) * TM;
+  const int n0 = in / high * TN;
+  const int k16 = (a.k + 15) / 16 * 16, stages = (a.k + 127) / 128;
+  const int nr = min(TN, a.n - n0), mr = (int)min((int64_t)TM, a.M - m0);
+  const i32x4_t rw = range_words(a.w + (int64_t)n0 * a.ld_w, (uint32_t)((nr - 1) * a.ld_w + k16));
+  const i32x4_t rq = range_words(a.q + m0 * a.ld_q, (uint32_t)((mr - 1) * a.ld_q + k16));
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8_t*)lds;
+
+  // direct loads: instruction i = wave + 4*j fills rows 8*i .. 8*i + 7
+  const int lrow = wave * 8 + lane / 8, lpiece = ((lane % 8) ^ (lane / 8)) * 16;
+  uint32_t woff[TN / 32], qoff[TM / 32];
+#pragma unroll
+  for (int j = 0; j < TN / 32; ++j)
+    woff[j] = lrow + 32 * j < nr ? (uint32_t)((lrow + 32 * j) * a.ld_w) + (uint32_t)lpiece : kOut;
+#pragma unroll
+  for (int j = 0; j < TM / 32; ++j)
+    qoff[j] = lrow + 32 * j < mr ? (uint32_t)((lrow + 32 * j) * a.ld_q) + (uint32_t)lpiece : kOut;
+  auto issue = [&](int s) {
+    if (s >= stages) return;
+    const uint32_t buf = lds0 + (uint32_t)((s & 1) * SB + wave * 1024);
+    const uint32_t k = (uint32_t)s * 128u;
+    const bool in_row = (int)k + lpiece < k16;  // bytes past the row's last piece read as zero
+#pragma unroll
+    for (int j = 0; j < TN / 32; ++j) load_lds(rw, in_row ? woff[j] + k : kOut, buf + j * 4096);
+#pragma unroll
+    for (int j = 0; j < TM / 32; ++j) load_lds(rq, in_row ? qoff[j] + k : kOut, buf + TN * 128 + j * 4096);
+  };
+
+  // fragments: lane -> row lane % 32, 16 bytes at 32*step + 16*(lane/32)
+  const uint32_t frow = (uint32_t)(lane % 32) * 128u;
+  uint4 fa[2][2][FN], fb[2][2][FM];  // [half parity][step of the half][fragment]
+  auto read = [&](int s, auto HALF) {
+    constexpr int half = decltype(HALF)::value;
+    const uint8_t* buf = lds + (s & 1) * SB;
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const uint32_t at = frow + (uint32_t)((((half * 2 + st) * 2 + lane / 32) ^ (lane % 8)) * 16);
+#pragma unroll
+      for (int f = 0; f < FN; ++f) fa[half][st][f] = ld16(buf + (wn * FN + f) * 4096 + at);
+#pragma unroll
+      for (int f = 0; f < FM; ++f) fb[half][st][f] = ld16(buf + TN * 128 + (wm * FM + f) * 4096 + at);
+    }
+  };
+  i32x16_t acc[FN][FM] = {};
+  auto products = [&](int s, auto HALF) {
+    constexpr int half = decltype(HALF)::value;
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const int k = s * 128 + (half * 2 + st) * 32 + lane / 32 * 16;
+      if (a.k % 16 && s == stages - 1) {  // the last piece's bytes past K count as zero
+#pragma unroll
+        for (int f = 0; f < FN; ++f) fa[half][st][f] = keep_bytes(fa[half][st][f], a.k - k);
+      }
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int g = 0; g < FM; ++g)
+          acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, fa[half][st][f]),
+                                                            __builtin_bit_cast(i32x4_t, fb[half][st][g]), acc[f][g], 0, 0, 0);
+    }
+  };
+
+  issue(0);
+  stage_landed();
+  lds_sync();
+  issue(1);
+  read(0, ic<0>{});
+  for (int s = 0; s < stages; ++s) {
+    read(s, ic<1>{});
+    products(s, ic<0>{});
+    stage_landed();
+    lds_sync();  // every wave has read stage s; stage s + 1 is in LDS
+    issue(s + 2);
+    if (s + 1 < stages) read(s + 1, ic<0>{});
+    products(s, ic<1>{});
+  }
+
+  // lane -> token lane % 32, channels 8*(i/4) + 4*(lane/32) + i % 4
+#pragma unroll
+  for (int f = 0; f < FN; ++f)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + (wn * FN + f) * 32 + q * 8 + lane / 32 * 4;
+      float ws[4], bias[4];
+      channel4<DT>(a, n, ws, bias);
+#pragma unroll
+      for (int g = 0; g < FM; ++g) {
+        const int64_t m = m0 + (wm * FM + g) * 32 + lane % 32;
+        if (m >= a.M || n >= a.n) continue;
+        const int v[4] = {acc[f][g][q * 4], acc[f][g][q * 4 + 1], acc[f][g][q * 4 + 2], acc[f][g][q * 4 + 3]};
+        store4<DT, VEC>(a, m, n, a.q_scale[m], ws, bias, v);
+      }
+    }
+}
+
+inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <int DT, int MT>
+int run_skinny(const LinearArgs& a, hipStream_t st) {
+  // as many channels a workgroup (at most 16) as fill the 256 CUs in whole rounds
+  const int rounds = (int)cdiv64(a.n, 256 * 16);
+  const int rows = (int)cdiv64(a.n, 256 * rounds);
+  const int units = (int)cdiv64(a.k, 128);
+  const int nw = units >= 48 ? 16 : units >= 8 ? 8 : 4;
+  const dim3 g((unsigned)cdiv64(a.n, rows), (unsigned)cdiv64(a.M, 16 * MT)), blk((unsigned)nw * 64);
+  const size_t lds = (size_t)nw * MT * 1024;
+  hipLaunchKernelGGL((linear_skinny<DT, MT, 4>), g, blk, lds, st, a, rows);
+  return (int)hipGetLastError();
+}
+
+template <int DT, int TM, int TN, bool VEC>
+int run_tile(const LinearArgs& a, hipStream_t st) {
+  const int tm = (int)cdiv64(a.M, TM), tn = (int)cdiv64(a.n, TN);
+  hipLaunchKernelGGL((linear_tile<DT, TM, TN, VEC>), dim3((unsigned)(cdiv64((int64_t)tm * tn, 8) * 8)), dim3(256),
+                     (2 * stage_bytes<TM, TN>()), st, a, tm, tn);
+  return (int)hipGetLastError();
+}
+
+template <int DT, bool VEC>
+int run_tiles(const LinearArgs& a, hipStream_t st) {
+  // the largest tile that still gives most CUs one
+  if (cdiv64(a.M, 256) * cdiv64(a.n, 256) >= 192) return run_tile<DT, 256, 256, VEC>(a, st);
+  if (cdiv64(a.M, 128) * cdiv64(a.n, 128) >= 192) return run_tile<DT, 128, 128, VEC>(a, st);
+  return run_tile<DT, 64, 64, VEC>(a, st);
+}
+
+template <int DT>
+int run(const LinearArgs& a, hipStream_t st) {
+  if (a.M <= 16) return run_skinny<DT, 1>(a, st);
+  if (a.M <= 32) return run_skinny<DT, 2>(a, st);
+  if (a.M <= 64) return run_skinny<DT, 4>(a, st);
+  const size_t b = DT == 2 ? 4 : 2;
+  const bool vec = a.n % 4 == 0 && a.ld_out % 4 == 0 && (uintptr_t)a.out % (4 * b) == 0;
+  return vec ? run_tiles<DT, true>(a, st) : run_tiles<DT, false>(a, st);
+}
+
+template <int DT>
+int raise_lds() {
+  const void* f[] = {(const void*)linear_tile<DT, 256, 256, true>, (const void*)linear_tile<DT, 256, 256, false>,
+                     (const void*)linear_skinny<DT, 4, 4>,         (const void*)linear_tile<DT, 128, 128, true>,
+                     (const void*)linear_tile<DT, 128, 128, false>};
+  for (const void* k : f) {
+    const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != hipSuccess) return (int)e;
+  }
+  return (int)hipSuccess;
 }
 
 }  // namespace
 
-int configure_linear_kernels() { return (int)hipSuccess; }
+// Raises the dynamic-LDS limit of the kernels on the current device.
+int configure_linear_kernels() {
+  for (int e : {raise_lds<0>(), raise_lds<1>(), raise_lds<2>()})
+    if (e != (int)hipSuccess) return e;
+  return (int)hipSuccess;
+}
 
 int launch_linear(const LinearArgs& args, int dtype, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const unsigned gx = (unsigned)((args.n + 63) / 64);
-  // the grid's second dimension holds 65535 tiles: larger M in several launches
-  constexpr int64_t kRows = (int64_t)65535 * 64;
+  // tile counts stay in 32 bits: larger M in several launches
+  constexpr int64_t kRows = (int64_t)1 << 20;
   const size_t b = dtype == 2 ? 4 : 2;
   for (int64_t m0 = 0; m0 < args.M; m0 += kRows) {
     LinearArgs a = args;
@@ -99,11 +369,7 @@ int launch_linear(const LinearArgs& args, int dtype, void* stream) {
     a.q += m0 * a.ld_q;
     a.q_scale += m0;
     a.out = reinterpret_cast<uint8_t*>(a.out) + (size_t)(m0 * a.ld_out) * b;
-    const dim3 g(gx, (unsigned)((a.M + 63) / 64)), blk(256);
-    if (dtype == 0) hipLaunchKernelGGL(linear_direct<0>, g, blk, 0, st, a);
-    else if (dtype == 1) hipLaunchKernelGGL(linear_direct<1>, g, blk, 0, st, a);
-    else hipLaunchKernelGGL(linear_direct<2>, g, blk, 0, st, a);
-    const int e = (int)hipGetLastError();
+    const int e = dtype == 0 ? run<0>(a, st) : dtype == 1 ? run<1>(a, st) : run<2>(a, st);
     if (e != (int)hipSuccess) return e;
   }
   return (int)hipSuccess;
