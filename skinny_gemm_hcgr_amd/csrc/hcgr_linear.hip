@@ -153,22 +153,30 @@ __global__ __launch_bounds__(1024) void linear_skinny(LinearArgs a, int rows) {
 }
 
 // ---------------------------------------------------------------------------
-// linear_tile: TM tokens x TN channels a workgroup, 4 waves as 2 x 2, each
-// (TM/2) x (TN/2) on v_mfma_i32_32x32x32_i8. K passes through LDS in stages of
-// 128 bytes a row, two buffers, written by direct loads: 1 KB an instruction,
-// 8 rows of 8 pieces, piece p of row r holding the row's piece p ^ (r % 8), so
-// that eight lanes reading one piece of eight rows meet every bank once. Half
-// a stage's fragments are read while the other half's products run; the one
-// barrier of a stage stands between its last read and the loads that reuse
-// its buffer, which have a whole stage's products to arrive in.
+// linear_tile: TM tokens x TN channels a tile, 4 waves as 2 x 2, each
+// (TM/2) x (TN/2) on v_mfma_i32_32x32x32_i8. K passes through a ring of NB
+// LDS buffers in stages of 64 bytes a row, written by direct loads: 1 KB an
+// instruction, 16 rows of 4 pieces, place p of row r holding the row's piece
+// p ^ (r/4 % 4), so that 16 lanes reading one piece of 16 rows meet every bank
+// once. A stage's fragments are read into registers while the products of the
+// stage before run, so its buffer is free one stage later and NB - 1 stages
+// of loads stay in flight. Workgroups are persistent: the loads run ahead
+// into the next tile, so that its first stages arrive behind this one's
+// epilogue. Past the last tile they are out of range and bring zeros. A tile's
+// scales come the same way. The epilogue turns the sums around in the one free
+// ring buffer, so that stores are whole 128-byte lines and nothing in it waits
+// for memory.
 // ---------------------------------------------------------------------------
 typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
-
 template <int N>
 using ic = std::integral_constant<int, N>;
 
 template <int TM, int TN>
-constexpr int stage_bytes() { return (TM + TN) * 128; }
+constexpr int stage_bytes() { return (TM + TN) * 64; }
+constexpr int kRing = 4;
+constexpr int kTables = 4096;  // [tile parity][w_scale, q_scale][256 floats]
+template <int TM, int TN>
+constexpr int tile_lds() { return kRing * stage_bytes<TM, TN>() + kTables; }
 
 // The four words of make_rsrc's descriptor.
 __device__ __forceinline__ i32x4_t range_words(const void* base, uint32_t bytes) {
@@ -178,122 +186,203 @@ __device__ __forceinline__ i32x4_t range_words(const void* base, uint32_t bytes)
 }
 // 1 KB from memory to LDS at `lds` (lane l's 16 bytes at lds + 16*l). Written
 // as assembly so that the compiler does not make every LDS read wait for all
-// loads in flight: the kernel waits itself (stage_landed). It writes no
-// registers but m0.
+// loads in flight: the kernel waits itself (landed). It writes no register but
+// m0, which nothing else in these kernels uses; m0 needs one wait state before
+// such a load.
 __device__ __forceinline__ void load_lds(i32x4_t r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                :
                : "v"(off), "s"(r), "s"(lds)
-               : "memory", "m0");
+               : "memory");
 }
-__device__ __forceinline__ void stage_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// The same, four bytes a lane (256 bytes).
+__device__ __forceinline__ void load_lds4(i32x4_t r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(r), "s"(lds)
+               : "memory");
+}
+// Until at most N of this wave's vector memory operations are outstanding.
+template <int N>
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
 template <int DT, int TM, int TN, bool VEC>
 __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile(LinearArgs a, int tiles_m, int tiles_n) {
   extern __shared__ uint8_t lds[];
-  constexpr int FM = TM / 64, FN = TN / 64, SB = stage_bytes<TM, TN>();
+  constexpr int FM = TM / 64, FN = TN / 64, SB = stage_bytes<TM, TN>(), NB = kRing;
+  constexpr int LW = TN / 64, LQ = TM / 64, L = LW + LQ;  // a wave's loads a stage
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
   const int wm = wave % 2, wn = wave / 2;
-  // Tiles in order: workgroups b, b + 8, b + 16, .. share an XCD and take
-  // neighbouring tiles, eight rows of tiles at a time, so that they meet in
-  // that XCD's L2.
+  // Workgroups b, b + 8, b + 16, .. share an XCD and take neighbouring tiles,
+  // eight rows of tiles at a time, so that they meet in that XCD's L2.
   const int tiles = tiles_m * tiles_n, per = (tiles + 7) / 8;
-  const int tile = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if ((int)(blockIdx.x / 8) >= per || tile >= tiles) return;  // the whole workgroup
-  const int band = tile / (8 * tiles_n), in = tile % (8 * tiles_n), high = min(8, tiles_m - band * 8);
-  const int64_t m0 = (int64_t)(band * 8 + in % high) * TM;
-  const int n0 = in / high * TN;
-  const int k16 = (a.k + 15) / 16 * 16, stages = (a.k + 127) / 128;
-  const int nr = min(TN, a.n - n0), mr = (int)min((int64_t)TM, a.M - m0);
-  const i32x4_t rw = range_words(a.w + (int64_t)n0 * a.ld_w, (uint32_t)((nr - 1) * a.ld_w + k16));
-  const i32x4_t rq = range_words(a.q + m0 * a.ld_q, (uint32_t)((mr - 1) * a.ld_q + k16));
+  const int first = (int)blockIdx.x / 8, stride = (int)gridDim.x / 8;
+  auto place = [&](int j, int64_t& m0, int& n0) {  // the workgroup's tile j; false past the last
+    const int local = first + j * stride, tile = (int)(blockIdx.x % 8) * per + local;
+    if (local >= per || tile >= tiles) return false;
+    const int band = tile / (8 * tiles_n), in = tile % (8 * tiles_n), high = min(8, tiles_m - band * 8);
+    m0 = (int64_t)(band * 8 + in % high) * TM;
+    n0 = in / high * TN;
+    return true;
+  };
+  const int k16 = (a.k + 15) / 16 * 16, stages = (a.k + 127) / 128 * 2;  // an even count: the last may be empty
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8_t*)lds;
 
-  // direct loads: instruction i = wave + 4*j fills rows 8*i .. 8*i + 7
-  const int lrow = wave * 8 + lane / 8, lpiece = ((lane % 8) ^ (lane / 8)) * 16;
-  uint32_t woff[TN / 32], qoff[TM / 32];
+  // Loads: instruction i = wave + 4*j fills rows 16*i .. 16*i + 15. Rows past
+  // the matrix are past the range (a pitch is at least k16).
+  const int lrow = wave * 16 + lane / 4, lpiece = ((lane % 4) ^ (lane / 16)) * 16;
+  uint32_t woff[LW], qoff[LQ];
 #pragma unroll
-  for (int j = 0; j < TN / 32; ++j)
-    woff[j] = lrow + 32 * j < nr ? (uint32_t)((lrow + 32 * j) * a.ld_w) + (uint32_t)lpiece : kOut;
+  for (int j = 0; j < LW; ++j) woff[j] = (uint32_t)((lrow + 64 * j) * a.ld_w) + (uint32_t)lpiece;
 #pragma unroll
-  for (int j = 0; j < TM / 32; ++j)
-    qoff[j] = lrow + 32 * j < mr ? (uint32_t)((lrow + 32 * j) * a.ld_q) + (uint32_t)lpiece : kOut;
-  auto issue = [&](int s) {
-    if (s >= stages) return;
-    const uint32_t buf = lds0 + (uint32_t)((s & 1) * SB + wave * 1024);
-    const uint32_t k = (uint32_t)s * 128u;
+  for (int j = 0; j < LQ; ++j) qoff[j] = (uint32_t)((lrow + 64 * j) * a.ld_q) + (uint32_t)lpiece;
+  const int8_t *wbase = a.w, *qbase = a.q;
+  uint32_t wbytes = 0, qbytes = 0;
+  int lt = 0, ls = 0;  // the next stage to load: of the workgroup's tile lt, stage ls
+  auto aim = [&]() {
+    int64_t m0 = 0;
+    int n0 = 0;
+    const bool in = place(lt, m0, n0);
+    const int nr = min(TN, a.n - n0), mr = (int)min((int64_t)TM, a.M - m0);
+    wbase = a.w + (int64_t)n0 * a.ld_w;
+    qbase = a.q + m0 * a.ld_q;
+    wbytes = in ? (uint32_t)((nr - 1) * a.ld_w + k16) : 0u;
+    qbytes = in ? (uint32_t)((mr - 1) * a.ld_q + k16) : 0u;
+  };
+  auto issue = [&](int slot) {
+    if (ls == 0) {  // the tile's scales
+      int64_t m0 = 0;
+      int n0 = 0;
+      const bool in = place(lt, m0, n0);
+      const uint32_t at = (uint32_t)(wave * 64 + lane) * 4u, to = lds0 + NB * SB + (lt & 1) * 2048 + wave * 256;
+      load_lds4(range_words(a.w_scale + n0, in ? (uint32_t)min(TN, a.n - n0) * 4u : 0u), at, to);
+      load_lds4(range_words(a.q_scale + m0, in ? (uint32_t)min((int64_t)TM, a.M - m0) * 4u : 0u), at, to + 1024);
+    }
+    const uint32_t buf = lds0 + (uint32_t)(slot * SB + wave * 1024), k = (uint32_t)ls * 64u;
     const bool in_row = (int)k + lpiece < k16;  // bytes past the row's last piece read as zero
+    const i32x4_t rw = range_words(wbase, wbytes), rq = range_words(qbase, qbytes);
 #pragma unroll
-    for (int j = 0; j < TN / 32; ++j) load_lds(rw, in_row ? woff[j] + k : kOut, buf + j * 4096);
+    for (int j = 0; j < LW; ++j) load_lds(rw, in_row ? woff[j] + k : kOut, buf + j * 4096);
 #pragma unroll
-    for (int j = 0; j < TM / 32; ++j) load_lds(rq, in_row ? qoff[j] + k : kOut, buf + TN * 128 + j * 4096);
+    for (int j = 0; j < LQ; ++j) load_lds(rq, in_row ? qoff[j] + k : kOut, buf + TN * 64 + j * 4096);
+    if (++ls == stages) {
+      ls = 0;
+      ++lt;
+      aim();
+    }
   };
 
   // fragments: lane -> row lane % 32, 16 bytes at 32*step + 16*(lane/32)
-  const uint32_t frow = (uint32_t)(lane % 32) * 128u;
-  uint4 fa[2][2][FN], fb[2][2][FM];  // [half parity][step of the half][fragment]
-  auto read = [&](int s, auto HALF) {
-    constexpr int half = decltype(HALF)::value;
-    const uint8_t* buf = lds + (s & 1) * SB;
+  uint4 fa[2][2][FN], fb[2][2][FM];  // [stage parity][step][fragment]
+  const uint32_t frow = (uint32_t)(lane % 32) * 64u;
+  auto read = [&](int slot, auto P) {
+    constexpr int p = decltype(P)::value;
+    const uint8_t* buf = lds + slot * SB;
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-      const uint32_t at = frow + (uint32_t)((((half * 2 + st) * 2 + lane / 32) ^ (lane % 8)) * 16);
+      const uint32_t at = frow + (uint32_t)(((st * 2 + lane / 32) ^ (lane / 4 % 4)) * 16);
 #pragma unroll
-      for (int f = 0; f < FN; ++f) fa[half][st][f] = ld16(buf + (wn * FN + f) * 4096 + at);
+      for (int f = 0; f < FN; ++f) fa[p][st][f] = ld16(buf + (wn * FN + f) * 2048 + at);
 #pragma unroll
-      for (int f = 0; f < FM; ++f) fb[half][st][f] = ld16(buf + TN * 128 + (wm * FM + f) * 4096 + at);
+      for (int f = 0; f < FM; ++f) fb[p][st][f] = ld16(buf + TN * 64 + (wm * FM + f) * 2048 + at);
     }
   };
-  i32x16_t acc[FN][FM] = {};
-  auto products = [&](int s, auto HALF) {
-    constexpr int half = decltype(HALF)::value;
+  i32x16_t acc[FN][FM];
+  const int tail = a.k % 16 ? a.k / 64 : -1;  // the stage whose last piece holds bytes past K
+  auto products = [&](int s, auto P, auto ZERO) {
+    constexpr int p = decltype(P)::value;
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-      const int k = s * 128 + (half * 2 + st) * 32 + lane / 32 * 16;
-      if (a.k % 16 && s == stages - 1) {  // the last piece's bytes past K count as zero
+      if (s == tail) {  // they count as zero
 #pragma unroll
-        for (int f = 0; f < FN; ++f) fa[half][st][f] = keep_bytes(fa[half][st][f], a.k - k);
+        for (int f = 0; f < FN; ++f) fa[p][st][f] = keep_bytes(fa[p][st][f], a.k - s * 64 - st * 32 - lane / 32 * 16);
       }
 #pragma unroll
       for (int f = 0; f < FN; ++f)
 #pragma unroll
         for (int g = 0; g < FM; ++g)
-          acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, fa[half][st][f]),
-                                                            __builtin_bit_cast(i32x4_t, fb[half][st][g]), acc[f][g], 0, 0, 0);
+          acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+              __builtin_bit_cast(i32x4_t, fa[p][st][f]), __builtin_bit_cast(i32x4_t, fb[p][st][g]),
+              decltype(ZERO)::value && st == 0 ? i32x16_t{} : acc[f][g], 0, 0, 0);
     }
   };
+  int cur = 0;  // slot of the stage whose products come next
+  // The slot of the stage just read takes the stage NB further on, and the
+  // next stage's fragments come in.
+  auto advance = [&](auto P) {
+    issue(cur);
+    cur = cur + 1 == NB ? 0 : cur + 1;
+    read(cur, P);
+  };
+  auto step = [&](int s, auto P, auto ZERO, auto LAST) {
+    // Every wave has read stage s (into registers), and stage s + 1 has
+    // landed: NB - 2 younger stages may be in flight (a store of an epilogue
+    // among them only lengthens the wait).
+    landed<(NB - 2) * L>();
+    lds_sync();
+    if constexpr (!decltype(LAST)::value) advance(ic<1 - decltype(P)::value>{});
+    products(s, P, ZERO);
+  };
 
-  issue(0);
-  stage_landed();
+  aim();
+  for (int i = 0; i < NB; ++i) issue(i);
+  landed<(NB - 1) * L>();
   lds_sync();
-  issue(1);
   read(0, ic<0>{});
-  for (int s = 0; s < stages; ++s) {
-    read(s, ic<1>{});
-    products(s, ic<0>{});
-    stage_landed();
-    lds_sync();  // every wave has read stage s; stage s + 1 is in LDS
-    issue(s + 2);
-    if (s + 1 < stages) read(s + 1, ic<0>{});
-    products(s, ic<1>{});
-  }
-
-  // lane -> token lane % 32, channels 8*(i/4) + 4*(lane/32) + i % 4
-#pragma unroll
-  for (int f = 0; f < FN; ++f)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + (wn * FN + f) * 32 + q * 8 + lane / 32 * 4;
-      float ws[4], bias[4];
-      channel4<DT>(a, n, ws, bias);
-#pragma unroll
-      for (int g = 0; g < FM; ++g) {
-        const int64_t m = m0 + (wm * FM + g) * 32 + lane % 32;
-        if (m >= a.M || n >= a.n) continue;
-        const int v[4] = {acc[f][g][q * 4], acc[f][g][q * 4 + 1], acc[f][g][q * 4 + 2], acc[f][g][q * 4 + 3]};
-        store4<DT, VEC>(a, m, n, a.q_scale[m], ws, bias, v);
-      }
+  int64_t m0 = 0;
+  int n0 = 0;
+  for (int j = 0; place(j, m0, n0); ++j) {
+    step(0, ic<0>{}, ic<1>{}, ic<0>{});
+    for (int s = 1; s + 1 < stages; s += 2) {
+      step(s, ic<1>{}, ic<0>{}, ic<0>{});
+      step(s + 1, ic<0>{}, ic<0>{}, ic<0>{});
     }
+    step(stages - 1, ic<1>{}, ic<0>{}, ic<1>{});
+    // Sums: lane -> token lane % 32, channels 8*(i/4) + 4*(lane/32) + i % 4.
+    // Through the wave's quarter of slot `cur`, which every wave has read:
+    // ROWS tokens x COLS channels a pass, a row's 16-byte places xored with
+    // the row.
+    constexpr int COLS = TN / 2 < 64 ? TN / 2 : 64, ROWS = SB / 4 / (COLS * 4), P = COLS / 4;
+    uint8_t* turn = lds + cur * SB + wave * (SB / 4);
+    const float* table = reinterpret_cast<const float*>(lds + NB * SB + (j & 1) * 2048);
+#pragma unroll
+    for (int h = 0; h < TN / 2 / COLS; ++h) {
+      const int nl = wn * (TN / 2) + h * COLS + lane % P * 4, n = n0 + nl;
+      float ws[4], bias[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ws[i] = table[nl + i];
+        bias[i] = a.bias && n + i < a.n ? bias_at<DT>(a.bias, n + i) : 0.0f;
+      }
+#pragma unroll
+      for (int g = 0; g < FM; ++g)
+#pragma unroll
+        for (int part = 0; part < 32 / ROWS; ++part) {
+          if (lane % 32 / ROWS == part) {
+#pragma unroll
+            for (int f = 0; f < COLS / 32; ++f)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const i32x16_t& c = acc[h * (COLS / 32) + f][g];
+                const int place16 = (f * 8 + q * 2 + lane / 32) ^ (lane % P);
+                *reinterpret_cast<i32x4_t*>(turn + (lane % ROWS) * (COLS * 4) + place16 * 16) =
+                    i32x4_t{c[q * 4], c[q * 4 + 1], c[q * 4 + 2], c[q * 4 + 3]};
+              }
+          }
+#pragma unroll
+          for (int k = 0; k < ROWS * P / 64; ++k) {
+            const int row = k * (64 / P) + lane / P;
+            const i32x4_t c = *reinterpret_cast<const i32x4_t*>(turn + row * (COLS * 4) + ((lane % P) ^ (row % P)) * 16);
+            const int ml = wm * (TM / 2) + g * 32 + part * ROWS + row;
+            const int v[4] = {c[0], c[1], c[2], c[3]};
+            if (m0 + ml < a.M && n < a.n) store4<DT, VEC>(a, m0 + ml, n, table[256 + ml], ws, bias, v);
+          }
+        }
+    }
+    lds_sync();  // every wave is done with the slot
+    advance(ic<0>{});
+  }
+  landed<0>();  // no load into this workgroup's LDS outlives it
 }
 
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -314,8 +403,11 @@ int run_skinny(const LinearArgs& a, hipStream_t st) {
 template <int DT, int TM, int TN, bool VEC>
 int run_tile(const LinearArgs& a, hipStream_t st) {
   const int tm = (int)cdiv64(a.M, TM), tn = (int)cdiv64(a.n, TN);
-  hipLaunchKernelGGL((linear_tile<DT, TM, TN, VEC>), dim3((unsigned)(cdiv64((int64_t)tm * tn, 8) * 8)), dim3(256),
-                     (2 * stage_bytes<TM, TN>()), st, a, tm, tn);
+  // persistent workgroups: as many as the 256 CUs hold at once
+  constexpr int kHeld = TM * TN >= 256 * 256 ? 256 : 512;
+  const int64_t tiles = cdiv64((int64_t)tm * tn, 8) * 8;
+  hipLaunchKernelGGL((linear_tile<DT, TM, TN, VEC>), dim3((unsigned)(tiles < kHeld ? tiles : kHeld)), dim3(256),
+                     (tile_lds<TM, TN>()), st, a, tm, tn);
   return (int)hipGetLastError();
 }
 
