@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "hcgr_block.h"
 #include "hcgr_device.h"
@@ -170,6 +171,11 @@ __global__ __launch_bounds__(1024) void linear_skinny(LinearArgs a, int rows) {
 typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
 template <int N>
 using ic = std::integral_constant<int, N>;
+// f(ic<0>), f(ic<1>), .. f(ic<N - 1>)
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) { (f(ic<I>{}), ...); }
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) { each_of(f, std::make_integer_sequence<int, N>{}); }
 
 template <int TM, int TN>
 constexpr int stage_bytes() { return (TM + TN) * 64; }
@@ -249,8 +255,27 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
     wbytes = in ? (uint32_t)((nr - 1) * a.ld_w + k16) : 0u;
     qbytes = in ? (uint32_t)((mr - 1) * a.ld_q + k16) : 0u;
   };
-  auto issue = [&](int slot) {
-    if (ls == 0) {  // the tile's scales
+  struct Loads {  // one stage's loads
+    i32x4_t rw, rq;
+    uint32_t buf, k;
+    bool in_row;
+  };
+  auto loads_into = [&](int slot) {
+    Loads z;
+    z.rw = range_words(wbase, wbytes);
+    z.rq = range_words(qbase, qbytes);
+    z.buf = lds0 + (uint32_t)(slot * SB + wave * 1024);
+    z.k = (uint32_t)ls * 64u;
+    z.in_row = (int)z.k + lpiece < k16;  // bytes past the row's last piece read as zero
+    return z;
+  };
+  auto load_one = [&](const Loads& z, auto I) {  // the i-th of a stage's L loads
+    constexpr int i = decltype(I)::value;
+    if constexpr (i < LW) load_lds(z.rw, z.in_row ? woff[i] + z.k : kOut, z.buf + i * 4096);
+    else load_lds(z.rq, z.in_row ? qoff[i - LW] + z.k : kOut, z.buf + TN * 64 + (i - LW) * 4096);
+  };
+  auto loaded = [&]() {  // on to the next stage; after a tile's first stage, its scales
+    if (ls == 0) {
       int64_t m0 = 0;
       int n0 = 0;
       const bool in = place(lt, m0, n0);
@@ -258,77 +283,78 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
       load_lds4(range_words(a.w_scale + n0, in ? (uint32_t)min(TN, a.n - n0) * 4u : 0u), at, to);
       load_lds4(range_words(a.q_scale + m0, in ? (uint32_t)min((int64_t)TM, a.M - m0) * 4u : 0u), at, to + 1024);
     }
-    const uint32_t buf = lds0 + (uint32_t)(slot * SB + wave * 1024), k = (uint32_t)ls * 64u;
-    const bool in_row = (int)k + lpiece < k16;  // bytes past the row's last piece read as zero
-    const i32x4_t rw = range_words(wbase, wbytes), rq = range_words(qbase, qbytes);
-#pragma unroll
-    for (int j = 0; j < LW; ++j) load_lds(rw, in_row ? woff[j] + k : kOut, buf + j * 4096);
-#pragma unroll
-    for (int j = 0; j < LQ; ++j) load_lds(rq, in_row ? qoff[j] + k : kOut, buf + TN * 64 + j * 4096);
     if (++ls == stages) {
       ls = 0;
       ++lt;
       aim();
     }
   };
+  auto issue = [&](int slot) {
+    const Loads z = loads_into(slot);
+    each<L>([&](auto I) { load_one(z, I); });
+    loaded();
+  };
 
   // fragments: lane -> row lane % 32, 16 bytes at 32*step + 16*(lane/32)
   uint4 fa[2][2][FN], fb[2][2][FM];  // [stage parity][step][fragment]
   const uint32_t frow = (uint32_t)(lane % 32) * 64u;
-  auto read = [&](int slot, auto P) {
-    constexpr int p = decltype(P)::value;
-    const uint8_t* buf = lds + slot * SB;
+  constexpr int R = 2 * (FN + FM);  // a wave's reads a stage
+  uint32_t fat[2];
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      const uint32_t at = frow + (uint32_t)(((st * 2 + lane / 32) ^ (lane / 4 % 4)) * 16);
-#pragma unroll
-      for (int f = 0; f < FN; ++f) fa[p][st][f] = ld16(buf + (wn * FN + f) * 2048 + at);
-#pragma unroll
-      for (int f = 0; f < FM; ++f) fb[p][st][f] = ld16(buf + TN * 64 + (wm * FM + f) * 2048 + at);
-    }
+  for (int st = 0; st < 2; ++st) fat[st] = frow + (uint32_t)(((st * 2 + lane / 32) ^ (lane / 4 % 4)) * 16);
+  auto read_one = [&](int slot, auto P, auto I) {  // the i-th of them
+    constexpr int p = decltype(P)::value, st = decltype(I)::value / (FN + FM), f = decltype(I)::value % (FN + FM);
+    const uint8_t* buf = lds + slot * SB + fat[st];
+    if constexpr (f < FN) fa[p][st][f] = ld16(buf + (wn * FN + f) * 2048);
+    else fb[p][st][f - FN] = ld16(buf + TN * 64 + (wm * FM + f - FN) * 2048);
   };
   i32x16_t acc[FN][FM];
   const int tail = a.k % 16 ? a.k / 64 : -1;  // the stage whose last piece holds bytes past K
-  auto products = [&](int s, auto P, auto ZERO) {
-    constexpr int p = decltype(P)::value;
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      if (s == tail) {  // they count as zero
-#pragma unroll
-        for (int f = 0; f < FN; ++f) fa[p][st][f] = keep_bytes(fa[p][st][f], a.k - s * 64 - st * 32 - lane / 32 * 16);
-      }
-#pragma unroll
-      for (int f = 0; f < FN; ++f)
-#pragma unroll
-        for (int g = 0; g < FM; ++g)
-          acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
-              __builtin_bit_cast(i32x4_t, fa[p][st][f]), __builtin_bit_cast(i32x4_t, fb[p][st][g]),
-              decltype(ZERO)::value && st == 0 ? i32x16_t{} : acc[f][g], 0, 0, 0);
-    }
-  };
   int cur = 0;  // slot of the stage whose products come next
-  // The slot of the stage just read takes the stage NB further on, and the
-  // next stage's fragments come in.
-  auto advance = [&](auto P) {
-    issue(cur);
-    cur = cur + 1 == NB ? 0 : cur + 1;
-    read(cur, P);
-  };
   auto step = [&](int s, auto P, auto ZERO, auto LAST) {
+    constexpr int p = decltype(P)::value;
     // Every wave has read stage s (into registers), and stage s + 1 has
     // landed: NB - 2 younger stages may be in flight (a store of an epilogue
     // among them only lengthens the wait).
     landed<(NB - 2) * L>();
     lds_sync();
-    if constexpr (!decltype(LAST)::value) advance(ic<1 - decltype(P)::value>{});
-    products(s, P, ZERO);
+    if (s == tail) {  // bytes past K count as zero
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int f = 0; f < FN; ++f) fa[p][st][f] = keep_bytes(fa[p][st][f], a.k - s * 64 - st * 32 - lane / 32 * 16);
+    }
+    // Stage s's slot takes the stage NB further on, and the next stage's
+    // fragments come in: these reads and loads are spread over the products,
+    // which would otherwise wait while a wave issues them.
+    const Loads z = loads_into(cur);
+    const int next = cur + 1 == NB ? 0 : cur + 1;
+    constexpr int NM = 2 * FN * FM, NO = decltype(LAST)::value ? 0 : R + L;
+    __builtin_amdgcn_sched_barrier(0);
+    each<NM>([&](auto T) {
+      constexpr int t = decltype(T)::value, st = t / (FN * FM), f = t / FM % FN, g = t % FM;
+      acc[f][g] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+          __builtin_bit_cast(i32x4_t, fa[p][st][f]), __builtin_bit_cast(i32x4_t, fb[p][st][g]),
+          decltype(ZERO)::value && st == 0 ? i32x16_t{} : acc[f][g], 0, 0, 0);
+      constexpr int o0 = t * NO / NM, o1 = (t + 1) * NO / NM;
+      each<o1 - o0>([&](auto O) {
+        constexpr int o = o0 + decltype(O)::value;
+        if constexpr (o < R) read_one(next, ic<1 - p>{}, ic<o>{});
+        else load_one(z, ic<o - R>{});
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (!decltype(LAST)::value) {
+      cur = next;
+      loaded();
+    }
   };
 
   aim();
   for (int i = 0; i < NB; ++i) issue(i);
   landed<(NB - 1) * L>();
   lds_sync();
-  read(0, ic<0>{});
+  each<R>([&](auto I) { read_one(0, ic<0>{}, I); });
   int64_t m0 = 0;
   int n0 = 0;
   for (int j = 0; place(j, m0, n0); ++j) {
@@ -380,7 +406,9 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
         }
     }
     lds_sync();  // every wave is done with the slot
-    advance(ic<0>{});
+    issue(cur);
+    cur = cur + 1 == NB ? 0 : cur + 1;
+    each<R>([&](auto I) { read_one(cur, ic<0>{}, I); });
   }
   landed<0>();  // no load into this workgroup's LDS outlives it
 }
