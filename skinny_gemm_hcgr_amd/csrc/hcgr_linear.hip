@@ -82,59 +82,115 @@ __device__ __forceinline__ void channel4(const LinearArgs& a, int n, float (&ws)
   }
 }
 
+template <int N>
+using ic = std::integral_constant<int, N>;
+// f(ic<0>), f(ic<1>), .. f(ic<N - 1>)
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) { (f(ic<I>{}), ...); }
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) { each_of(f, std::make_integer_sequence<int, N>{}); }
+
+// The four words of make_rsrc's descriptor.
+__device__ __forceinline__ i32x4_t range_words(const void* base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)p), __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xffff),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// 1 KB from memory to LDS at `lds` (lane l's 16 bytes at lds + 16*l). Written
+// as assembly so that the compiler does not make every LDS read wait for all
+// loads in flight: the kernel waits itself (landed). It writes no register but
+// m0, which nothing else in these kernels uses; m0 needs one wait state before
+// such a load.
+__device__ __forceinline__ void load_lds(i32x4_t r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(r), "s"(lds)
+               : "memory");
+}
+// The same, four bytes a lane (256 bytes).
+__device__ __forceinline__ void load_lds4(i32x4_t r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(r), "s"(lds)
+               : "memory");
+}
+// Until at most N of this wave's vector memory operations are outstanding.
+template <int N>
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
+
 // ---------------------------------------------------------------------------
 // linear_skinny: up to 16*MT tokens. The product streams the weights once, so
-// it is bound by their bytes: a workgroup owns `rows` (1..16) output channels,
-// its waves share K in units of 128 bytes (a wave's loads cover whole lines of
-// its rows), and the operands go straight from memory into MFMA registers,
-// U units of weights ahead. The waves' sums meet in LDS.
+// it is bound by their bytes, and by the tokens, which every CU reads whole: a
+// workgroup owns `rows` (1..16) output channels, and its waves share K in
+// units of 128 bytes. Each wave runs a ring of D units of its own in LDS,
+// without barriers: 16 rows of weights and 16*MT of tokens, 1 KB a direct
+// load, 8 rows of 8 pieces (a row's line by neighbouring lanes: fragments
+// loaded straight into registers ask for 16 bytes of 16 lines at a time, which
+// took the address units four times as long), place p of row r holding piece
+// p ^ (r/2 % 8), so that 16 lanes reading one piece of 16 rows meet every bank
+// once. The waves' sums meet in LDS.
 // ---------------------------------------------------------------------------
-template <int DT, int MT, int U>
-__global__ __launch_bounds__(1024) void linear_skinny(LinearArgs a, int rows) {
-  extern __shared__ int32_t part[];  // [waves][MT][64 lanes][4]
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, nw = (int)blockDim.x / 64;
-  const int r16 = lane % 16, kq = lane / 16;
+template <int DT, int MT, int D>
+__global__ __launch_bounds__(512) void linear_skinny(LinearArgs a, int rows) {
+  extern __shared__ uint8_t lds[];
+  constexpr int L = 2 + 2 * MT, UB = L * 1024;  // a unit's loads and bytes
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+  const int nw = (int)blockDim.x / 64, r16 = lane % 16, kq = lane / 16;
   const int n0 = (int)blockIdx.x * rows;
   const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
   const int k16 = (a.k + 15) / 16 * 16, units = (a.k + 127) / 128;
   const int nr = min(rows, a.n - n0), mr = (int)min((int64_t)(16 * MT), a.M - m0);
-  const rsrc_t rw = make_rsrc(a.w + (int64_t)n0 * a.ld_w, (uint32_t)((nr - 1) * a.ld_w + k16));
-  const rsrc_t rq = make_rsrc(a.q + m0 * a.ld_q, (uint32_t)((mr - 1) * a.ld_q + k16));
-  // rows past the last and bytes past the row's last piece read as zero
-  const uint32_t wrow = r16 < nr ? (uint32_t)(r16 * a.ld_w) : kOut;
-  uint32_t qrow[MT];
+  // rows past the last are past the range (a pitch is at least k16)
+  const i32x4_t rw = range_words(a.w + (int64_t)n0 * a.ld_w, (uint32_t)((nr - 1) * a.ld_w + k16));
+  const i32x4_t rq = range_words(a.q + m0 * a.ld_q, (uint32_t)((mr - 1) * a.ld_q + k16));
+  uint8_t* ring = lds + wave * (D * UB);
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(lds_u8_t*)lds + (uint32_t)(wave * (D * UB));
+  // load i of a matrix fills rows 8*i .. 8*i + 7; the piece's place depends on i's parity
+  const int lr = lane / 8;
+  const uint32_t piece[2] = {(uint32_t)((lane % 8) ^ (lr / 2)) * 16u, (uint32_t)((lane % 8) ^ (4 + lr / 2)) * 16u};
+  uint32_t woff[2], qoff[2 * MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) qrow[t] = t * 16 + r16 < mr ? (uint32_t)((t * 16 + r16) * a.ld_q) : kOut;
+  for (int i = 0; i < 2; ++i) woff[i] = (uint32_t)((8 * i + lr) * a.ld_w) + piece[i];
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) qoff[i] = (uint32_t)((8 * i + lr) * a.ld_q) + piece[i % 2];
+  auto issue = [&](int u, int slot) {  // unit u of K; past the last, or past the row's last piece: zeros
+    const uint32_t k = (uint32_t)u * 128u, buf = ring0 + (uint32_t)(slot * UB);
+    const bool in[2] = {(int)(k + piece[0]) < k16, (int)(k + piece[1]) < k16};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_lds(rw, in[i] ? woff[i] + k : kOut, buf + i * 1024);
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) load_lds(rq, in[i % 2] ? qoff[i] + k : kOut, buf + 2048 + i * 1024);
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) issue(wave + i * nw, i);
+  const uint32_t at = (uint32_t)(r16 * 128), key = (uint32_t)(r16 / 2 % 8);
   i32x4_t acc[MT] = {};
-  for (int u0 = wave; u0 < units; u0 += nw * U) {
-    uint4 w[U][2], x[2][MT][2];
+  int slot = 0;
+  for (int u = wave; u < units; u += nw) {
+    landed<(D - 1) * L>();
+    const uint8_t* buf = ring + slot * UB;
+    uint4 w[2], x[MT][2];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int k = (u0 + i * nw) * 128 + kq * 32;
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t o = at + (((uint32_t)(h * 4 + kq) ^ key) * 16u);
+      w[h] = ld16(buf + o);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) w[i][h] = bld16_nt(rw, k + 16 * h < k16 ? wrow + (uint32_t)(k + 16 * h) : kOut);
+      for (int t = 0; t < MT; ++t) x[t][h] = ld16(buf + 2048 + t * 2048 + o);
     }
-    auto load_x = [&](int i) {  // tokens: one unit ahead, they come from the caches
-      const int k = (u0 + i * nw) * 128 + kq * 32;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is read
+    issue(u + D * nw, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+    for (int h = 0; h < 2; ++h) {
+      const int k = u * 128 + h * 64 + kq * 16;
+      if (a.k % 16 && k + 16 > a.k) w[h] = keep_bytes(w[h], a.k - k);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          x[i % 2][t][h] = bld16(rq, k + 16 * h < k16 ? qrow[t] + (uint32_t)(k + 16 * h) : kOut);
-    };
-    load_x(0);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int k = (u0 + i * nw) * 128 + kq * 32;
-      if (i + 1 < U) load_x(i + 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (a.k % 16 && k + 16 * h + 16 > a.k) w[i][h] = keep_bytes(w[i][h], a.k - k - 16 * h);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[t] = mfma_i8(w[i][h], x[i % 2][t][h], acc[t]);
-      }
+      for (int t = 0; t < MT; ++t) acc[t] = mfma_i8(w[h], x[t][h], acc[t]);
     }
   }
+  landed<0>();
+  __syncthreads();  // the rings make room for the sums: [waves][MT][64 lanes][4]
+  int32_t* part = reinterpret_cast<int32_t*>(lds);
 #pragma unroll
   for (int t = 0; t < MT; ++t)
     *reinterpret_cast<i32x4_t*>(part + ((wave * MT + t) * 64 + lane) * 4) = acc[t];
@@ -169,48 +225,12 @@ __global__ __launch_bounds__(1024) void linear_skinny(LinearArgs a, int rows) {
 // for memory.
 // ---------------------------------------------------------------------------
 typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
-template <int N>
-using ic = std::integral_constant<int, N>;
-// f(ic<0>), f(ic<1>), .. f(ic<N - 1>)
-template <typename F, int... I>
-__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) { (f(ic<I>{}), ...); }
-template <int N, typename F>
-__device__ __forceinline__ void each(F f) { each_of(f, std::make_integer_sequence<int, N>{}); }
-
 template <int TM, int TN>
 constexpr int stage_bytes() { return (TM + TN) * 64; }
 constexpr int kRing = 4;
 constexpr int kTables = 4096;  // [tile parity][w_scale, q_scale][256 floats]
 template <int TM, int TN>
 constexpr int tile_lds() { return kRing * stage_bytes<TM, TN>() + kTables; }
-
-// The four words of make_rsrc's descriptor.
-__device__ __forceinline__ i32x4_t range_words(const void* base, uint32_t bytes) {
-  const uint64_t p = (uint64_t)(uintptr_t)base;
-  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)p), __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xffff),
-                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
-}
-// 1 KB from memory to LDS at `lds` (lane l's 16 bytes at lds + 16*l). Written
-// as assembly so that the compiler does not make every LDS read wait for all
-// loads in flight: the kernel waits itself (landed). It writes no register but
-// m0, which nothing else in these kernels uses; m0 needs one wait state before
-// such a load.
-__device__ __forceinline__ void load_lds(i32x4_t r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :
-               : "v"(off), "s"(r), "s"(lds)
-               : "memory");
-}
-// The same, four bytes a lane (256 bytes).
-__device__ __forceinline__ void load_lds4(i32x4_t r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :
-               : "v"(off), "s"(r), "s"(lds)
-               : "memory");
-}
-// Until at most N of this wave's vector memory operations are outstanding.
-template <int N>
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
 template <int DT, int TM, int TN, bool VEC>
 __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile(LinearArgs a, int tiles_m, int tiles_n) {
@@ -415,17 +435,23 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
 
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+template <int DT, int MT, int D>
+int launch_skinny(const LinearArgs& a, int rows, int nw, hipStream_t st) {
+  const dim3 g((unsigned)cdiv64(a.n, rows), (unsigned)cdiv64(a.M, 16 * MT)), blk((unsigned)nw * 64);
+  hipLaunchKernelGGL((linear_skinny<DT, MT, D>), g, blk, (size_t)nw * D * (2 + 2 * MT) * 1024, st, a, rows);
+  return (int)hipGetLastError();
+}
+
 template <int DT, int MT>
 int run_skinny(const LinearArgs& a, hipStream_t st) {
-  // as many channels a workgroup (at most 16) as fill the 256 CUs in whole rounds
-  const int rounds = (int)cdiv64(a.n, 256 * 16);
-  const int rows = (int)cdiv64(a.n, 256 * rounds);
-  const int units = (int)cdiv64(a.k, 128);
-  const int nw = units >= 48 ? 16 : units >= 8 ? 8 : 4;
-  const dim3 g((unsigned)cdiv64(a.n, rows), (unsigned)cdiv64(a.M, 16 * MT)), blk((unsigned)nw * 64);
-  const size_t lds = (size_t)nw * MT * 1024;
-  hipLaunchKernelGGL((linear_skinny<DT, MT, 4>), g, blk, lds, st, a, rows);
-  return (int)hipGetLastError();
+  // as many channels a workgroup (at most 16) as fill the 256 CUs in whole
+  // rounds; the rings of the workgroups that share a CU fill its LDS: one of
+  // eight waves, or two or three of four
+  const int rounds = (int)cdiv64(a.n, 256 * 16), rows = (int)cdiv64(a.n, 256 * rounds);
+  constexpr int kFew = MT == 1 ? 5 : MT == 2 ? 3 : 2, kMany = MT == 1 ? 3 : 2;
+  if (rounds == 1) return launch_skinny<DT, MT, kFew>(a, rows, 8, st);
+  if (rounds == 2) return launch_skinny<DT, MT, kFew>(a, rows, 4, st);
+  return launch_skinny<DT, MT, kMany>(a, rows, 4, st);
 }
 
 template <int DT, int TM, int TN, bool VEC>
@@ -460,8 +486,10 @@ int run(const LinearArgs& a, hipStream_t st) {
 template <int DT>
 int raise_lds() {
   const void* f[] = {(const void*)linear_tile<DT, 256, 256, true>, (const void*)linear_tile<DT, 256, 256, false>,
-                     (const void*)linear_skinny<DT, 4, 4>,         (const void*)linear_tile<DT, 128, 128, true>,
-                     (const void*)linear_tile<DT, 128, 128, false>};
+                     (const void*)linear_tile<DT, 128, 128, true>,
+                     (const void*)linear_tile<DT, 128, 128, false>, (const void*)linear_skinny<DT, 1, 5>,
+                     (const void*)linear_skinny<DT, 1, 3>,         (const void*)linear_skinny<DT, 2, 3>,
+                     (const void*)linear_skinny<DT, 2, 2>,         (const void*)linear_skinny<DT, 4, 2>};
   for (const void* k : f) {
     const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != hipSuccess) return (int)e;
