@@ -5,6 +5,7 @@
 // output channels of one token.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -46,10 +47,10 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v) {
 }
 
 // Four output channels n .. n+3 of token m from their sums. VEC: the row's
-// pieces of four values are aligned and whole.
+// pieces of four values are aligned and whole; otherwise those below `end`.
 template <int DT, bool VEC>
 __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int n, float qs, const float (&ws)[4],
-                                       const float (&bias)[4], const int (&acc)[4]) {
+                                       const float (&bias)[4], const int (&acc)[4], int end) {
   float v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = fmaf((float)acc[i], qs * ws[i], bias[i]);
@@ -68,7 +69,7 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int n, fl
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n + i < a.n) store1<DT>(a.out, at + i, v[i]);
+      if (n + i < end) store1<DT>(a.out, at + i, v[i]);
   }
 }
 // Scales and bias of channels n .. n+3 (zero past N).
@@ -119,25 +120,30 @@ template <int N>
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 
 // ---------------------------------------------------------------------------
-// linear_skinny: up to 16*MT tokens. The product streams the weights once, so
-// it is bound by their bytes, and by the tokens, which every CU reads whole: a
-// workgroup owns `rows` (1..16) output channels, and its waves share K in
-// units of 128 bytes. Each wave runs a ring of D units of its own in LDS,
-// without barriers: 16 rows of weights and 16*MT of tokens, 1 KB a direct
-// load, 8 rows of 8 pieces (a row's line by neighbouring lanes: fragments
-// loaded straight into registers ask for 16 bytes of 16 lines at a time, which
-// took the address units four times as long), place p of row r holding piece
-// p ^ (r/2 % 8), so that 16 lanes reading one piece of 16 rows meet every bank
-// once. The waves' sums meet in LDS.
+// linear_split: 16*MT tokens and `rows` (up to 16*NT) output channels a
+// workgroup, whose waves share K in units of 128 bytes. For few tokens the
+// product streams the weights once and is bound by their bytes, and by the
+// tokens, which every workgroup reads whole. Each wave runs a ring of D units
+// of its own in LDS, without barriers, 1 KB a direct load, 8 rows of 8 pieces
+// (a row's line by neighbouring lanes: fragments loaded straight into
+// registers ask for 16 bytes of 16 lines at a time, which took the address
+// units four times as long), place p of row r holding piece p ^ (r/2 % 8), so
+// that 16 lanes reading one piece of 16 rows meet every bank once. The waves'
+// sums meet in LDS.
 // ---------------------------------------------------------------------------
-template <int DT, int MT, int D>
-__global__ __launch_bounds__(512) void linear_skinny(LinearArgs a, int rows) {
+template <int DT, int MT, int NT, int D>
+__global__ __launch_bounds__(512) void linear_split(LinearArgs a, int rows, int tiles_m, int vec) {
   extern __shared__ uint8_t lds[];
-  constexpr int L = 2 + 2 * MT, UB = L * 1024;  // a unit's loads and bytes
+  constexpr int L = 2 * (NT + MT), UB = L * 1024;  // a unit's loads and bytes
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
   const int nw = (int)blockDim.x / 64, r16 = lane % 16, kq = lane / 16;
-  const int n0 = (int)blockIdx.x * rows;
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  // Workgroups b, b + 8, b + 16, .. share an XCD: those of one XCD take the
+  // tokens of the same channels one after the other, so that the weights come
+  // from memory once.
+  const int local = (int)blockIdx.x / 8;
+  const int n0 = (local / tiles_m * 8 + (int)blockIdx.x % 8) * rows;
+  if (n0 >= a.n) return;  // the whole workgroup
+  const int64_t m0 = (int64_t)(local % tiles_m) * (16 * MT);
   const int k16 = (a.k + 15) / 16 * 16, units = (a.k + 127) / 128;
   const int nr = min(rows, a.n - n0), mr = (int)min((int64_t)(16 * MT), a.M - m0);
   // rows past the last are past the range (a pitch is at least k16)
@@ -148,34 +154,35 @@ __global__ __launch_bounds__(512) void linear_skinny(LinearArgs a, int rows) {
   // load i of a matrix fills rows 8*i .. 8*i + 7; the piece's place depends on i's parity
   const int lr = lane / 8;
   const uint32_t piece[2] = {(uint32_t)((lane % 8) ^ (lr / 2)) * 16u, (uint32_t)((lane % 8) ^ (4 + lr / 2)) * 16u};
-  uint32_t woff[2], qoff[2 * MT];
+  uint32_t woff[2 * NT], qoff[2 * MT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) woff[i] = (uint32_t)((8 * i + lr) * a.ld_w) + piece[i];
+  for (int i = 0; i < 2 * NT; ++i) woff[i] = (uint32_t)((8 * i + lr) * a.ld_w) + piece[i % 2];
 #pragma unroll
   for (int i = 0; i < 2 * MT; ++i) qoff[i] = (uint32_t)((8 * i + lr) * a.ld_q) + piece[i % 2];
   auto issue = [&](int u, int slot) {  // unit u of K; past the last, or past the row's last piece: zeros
     const uint32_t k = (uint32_t)u * 128u, buf = ring0 + (uint32_t)(slot * UB);
     const bool in[2] = {(int)(k + piece[0]) < k16, (int)(k + piece[1]) < k16};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) load_lds(rw, in[i] ? woff[i] + k : kOut, buf + i * 1024);
+    for (int i = 0; i < 2 * NT; ++i) load_lds(rw, in[i % 2] ? woff[i] + k : kOut, buf + i * 1024);
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) load_lds(rq, in[i % 2] ? qoff[i] + k : kOut, buf + 2048 + i * 1024);
+    for (int i = 0; i < 2 * MT; ++i) load_lds(rq, in[i % 2] ? qoff[i] + k : kOut, buf + NT * 2048 + i * 1024);
   };
 #pragma unroll
   for (int i = 0; i < D; ++i) issue(wave + i * nw, i);
   const uint32_t at = (uint32_t)(r16 * 128), key = (uint32_t)(r16 / 2 % 8);
-  i32x4_t acc[MT] = {};
+  i32x4_t acc[NT][MT] = {};
   int slot = 0;
   for (int u = wave; u < units; u += nw) {
     landed<(D - 1) * L>();
     const uint8_t* buf = ring + slot * UB;
-    uint4 w[2], x[MT][2];
+    uint4 w[NT][2], x[MT][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t o = at + (((uint32_t)(h * 4 + kq) ^ key) * 16u);
-      w[h] = ld16(buf + o);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) x[t][h] = ld16(buf + 2048 + t * 2048 + o);
+      for (int t = 0; t < NT; ++t) w[t][h] = ld16(buf + t * 2048 + o);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) x[t][h] = ld16(buf + (NT + t) * 2048 + o);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is read
     issue(u + D * nw, slot);
@@ -183,29 +190,36 @@ __global__ __launch_bounds__(512) void linear_skinny(LinearArgs a, int rows) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = u * 128 + h * 64 + kq * 16;
-      if (a.k % 16 && k + 16 > a.k) w[h] = keep_bytes(w[h], a.k - k);
+      if (a.k % 16 && k + 16 > a.k) {  // bytes past K count as zero
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = mfma_i8(w[h], x[t][h], acc[t]);
+        for (int c = 0; c < NT; ++c) w[c][h] = keep_bytes(w[c][h], a.k - k);
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[c][t] = mfma_i8(w[c][h], x[t][h], acc[c][t]);
     }
   }
   landed<0>();
-  __syncthreads();  // the rings make room for the sums: [waves][MT][64 lanes][4]
+  __syncthreads();  // the rings make room for the sums: [waves][MT][NT][64 lanes][4]
   int32_t* part = reinterpret_cast<int32_t*>(lds);
 #pragma unroll
   for (int t = 0; t < MT; ++t)
-    *reinterpret_cast<i32x4_t*>(part + ((wave * MT + t) * 64 + lane) * 4) = acc[t];
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+      *reinterpret_cast<i32x4_t*>(part + (((wave * MT + t) * NT + c) * 64 + lane) * 4) = acc[c][t];
   __syncthreads();
-  // thread -> (token, channel); the sums of channel c of token t*16 + r are
-  // word c % 4 of lane (c/4)*16 + r
-  for (int i = threadIdx.x; i < 256 * MT; i += blockDim.x) {
-    const int c = i % 16, r = i / 16 % 16, t = i / 256;
-    if (c >= nr || t * 16 + r >= mr) continue;
-    int sum = 0;
-    for (int v = 0; v < nw; ++v) sum += part[((v * MT + t) * 64 + (c / 4) * 16 + r) * 4 + c % 4];
-    const int64_t m = m0 + t * 16 + r;
-    const int n = n0 + c;
-    const float b = a.bias ? bias_at<DT>(a.bias, n) : 0.0f;
-    store1<DT>(a.out, m * a.ld_out + n, fmaf((float)sum, a.q_scale[m] * a.w_scale[n], b));
+  // thread -> four neighbouring channels of a token, in the products' layout
+  for (int i = threadIdx.x; i < 64 * MT * NT; i += blockDim.x) {
+    const int c = i / 64 % NT * 16 + i % 64 / 16 * 4, r = i / (64 * NT) * 16 + i % 16;
+    if (c >= nr || r >= mr) continue;
+    i32x4_t sum = *reinterpret_cast<const i32x4_t*>(part + i * 4);
+    for (int v = 1; v < nw; ++v) sum += *reinterpret_cast<const i32x4_t*>(part + (v * MT * NT * 64 + i) * 4);
+    const int four[4] = {sum[0], sum[1], sum[2], sum[3]};
+    float ws[4], bias[4];
+    channel4<DT>(a, n0 + c, ws, bias);
+    if (vec) store4<DT, true>(a, m0 + r, n0 + c, a.q_scale[m0 + r], ws, bias, four, a.n);
+    else store4<DT, false>(a, m0 + r, n0 + c, a.q_scale[m0 + r], ws, bias, four, n0 + nr);
   }
 }
 
@@ -227,8 +241,8 @@ __global__ __launch_bounds__(512) void linear_skinny(LinearArgs a, int rows) {
 typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
 template <int TM, int TN>
 constexpr int stage_bytes() { return (TM + TN) * 64; }
-constexpr int kRing = 4;
 constexpr int kTables = 4096;  // [tile parity][w_scale, q_scale][256 floats]
+constexpr int kRing = 4;
 template <int TM, int TN>
 constexpr int tile_lds() { return kRing * stage_bytes<TM, TN>() + kTables; }
 
@@ -251,7 +265,9 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
     n0 = in / high * TN;
     return true;
   };
-  const int k16 = (a.k + 15) / 16 * 16, stages = (a.k + 127) / 128 * 2;  // an even count: the last may be empty
+  const int k16 = (a.k + 15) / 16 * 16, stages = max((a.k + 127) / 128 * 2, NB);
+  // (an even count, the last may be empty; not below NB, so that the loads run
+  // ahead by less than two tiles and two sets of scales suffice)
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8_t*)lds;
 
   // Loads: instruction i = wave + 4*j fills rows 16*i .. 16*i + 15. Rows past
@@ -421,7 +437,7 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
             const i32x4_t c = *reinterpret_cast<const i32x4_t*>(turn + row * (COLS * 4) + ((lane % P) ^ (row % P)) * 16);
             const int ml = wm * (TM / 2) + g * 32 + part * ROWS + row;
             const int v[4] = {c[0], c[1], c[2], c[3]};
-            if (m0 + ml < a.M && n < a.n) store4<DT, VEC>(a, m0 + ml, n, table[256 + ml], ws, bias, v);
+            if (m0 + ml < a.M && n < a.n) store4<DT, VEC>(a, m0 + ml, n, table[256 + ml], ws, bias, v, a.n);
           }
         }
     }
@@ -435,61 +451,78 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
 
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int DT, int MT, int D>
-int launch_skinny(const LinearArgs& a, int rows, int nw, hipStream_t st) {
-  const dim3 g((unsigned)cdiv64(a.n, rows), (unsigned)cdiv64(a.M, 16 * MT)), blk((unsigned)nw * 64);
-  hipLaunchKernelGGL((linear_skinny<DT, MT, D>), g, blk, (size_t)nw * D * (2 + 2 * MT) * 1024, st, a, rows);
+// Whether a row of out is whole, aligned pieces of four values.
+template <int DT>
+bool pieces_of_four(const LinearArgs& a) {
+  return a.n % 4 == 0 && a.ld_out % 4 == 0 && (uintptr_t)a.out % (DT == 2 ? 16 : 8) == 0;
+}
+
+template <int DT, int MT, int NT, int D>
+int launch_split(const LinearArgs& a, int rows, int nw, hipStream_t st) {
+  const int tm = (int)cdiv64(a.M, 16 * MT);
+  const dim3 g((unsigned)(cdiv64(cdiv64(a.n, rows), 8) * 8 * tm)), blk((unsigned)nw * 64);
+  hipLaunchKernelGGL((linear_split<DT, MT, NT, D>), g, blk, (size_t)nw * D * (MT + NT) * 2048, st, a, rows, tm,
+                     rows % 4 == 0 && pieces_of_four<DT>(a));
   return (int)hipGetLastError();
 }
 
+// Up to 16*MT tokens: as many channels a workgroup (at most 16) as fill the
+// 256 CUs in whole rounds; the rings of the workgroups that share a CU fill
+// its LDS: one of eight waves, or two or three of four.
 template <int DT, int MT>
 int run_skinny(const LinearArgs& a, hipStream_t st) {
-  // as many channels a workgroup (at most 16) as fill the 256 CUs in whole
-  // rounds; the rings of the workgroups that share a CU fill its LDS: one of
-  // eight waves, or two or three of four
   const int rounds = (int)cdiv64(a.n, 256 * 16), rows = (int)cdiv64(a.n, 256 * rounds);
-  constexpr int kFew = MT == 1 ? 5 : MT == 2 ? 3 : 2, kMany = MT == 1 ? 3 : 2;
-  if (rounds == 1) return launch_skinny<DT, MT, kFew>(a, rows, 8, st);
-  if (rounds == 2) return launch_skinny<DT, MT, kFew>(a, rows, 4, st);
-  return launch_skinny<DT, MT, kMany>(a, rows, 4, st);
+  constexpr int kFew = MT == 1 ? 5 : 3, kMany = MT == 1 ? 3 : 2;
+  if (rounds == 1) return launch_split<DT, MT, 1, kFew>(a, rows, 8, st);
+  if (rounds == 2) return launch_split<DT, MT, 1, kFew>(a, rows, 4, st);
+  return launch_split<DT, MT, 1, kMany>(a, rows, 4, st);
 }
 
 template <int DT, int TM, int TN, bool VEC>
-int run_tile(const LinearArgs& a, hipStream_t st) {
+int launch_tile(const LinearArgs& a, hipStream_t st) {
   const int tm = (int)cdiv64(a.M, TM), tn = (int)cdiv64(a.n, TN);
   // persistent workgroups: as many as the 256 CUs hold at once
   constexpr int kHeld = TM * TN >= 256 * 256 ? 256 : 512;
   const int64_t tiles = cdiv64((int64_t)tm * tn, 8) * 8;
-  hipLaunchKernelGGL((linear_tile<DT, TM, TN, VEC>), dim3((unsigned)(tiles < kHeld ? tiles : kHeld)), dim3(256),
+  hipLaunchKernelGGL((linear_tile<DT, TM, TN, VEC>), dim3((unsigned)std::min<int64_t>(tiles, kHeld)), dim3(256),
                      (tile_lds<TM, TN>()), st, a, tm, tn);
   return (int)hipGetLastError();
 }
-
-template <int DT, bool VEC>
-int run_tiles(const LinearArgs& a, hipStream_t st) {
-  // the largest tile that still gives most CUs one
-  if (cdiv64(a.M, 256) * cdiv64(a.n, 256) >= 192) return run_tile<DT, 256, 256, VEC>(a, st);
-  if (cdiv64(a.M, 128) * cdiv64(a.n, 128) >= 192) return run_tile<DT, 128, 128, VEC>(a, st);
-  return run_tile<DT, 64, 64, VEC>(a, st);
+template <int DT, int TM, int TN>
+int run_tile(const LinearArgs& a, hipStream_t st) {
+  return pieces_of_four<DT>(a) ? launch_tile<DT, TM, TN, true>(a, st) : launch_tile<DT, TM, TN, false>(a, st);
 }
 
+// The kernel is the one that a model of its time, in microseconds, puts first:
+// a start, then rounds of workgroups over the 256 CUs, each with a part of its
+// own and one for each unit of 128 bytes of K; the kernels for few tokens are
+// also bound by the weights' bytes at 5.2 TB/s. The constants are fitted on
+// one MI355X to N x K = 1024 x 1024 .. 10240 x 2560 and 2560 x 10240, M = 1 ..
+// 2048 (all within a quarter of the measured times). Measured, split 32x32 /
+// split 64x64 / tile 128 / tile 256: 2560x10240 at M = 64: 10.9 / 20 / 47 /
+// 101 us, M = 384: 33 / 21 / 51 / 107, M = 1024: - / 74 / 51 / 113; 10240x2560
+// at M = 384: 37 / 33 / 21 / 39, M = 3000: - / 179 / 116 / 92.
 template <int DT>
 int run(const LinearArgs& a, hipStream_t st) {
-  if (a.M <= 16) return run_skinny<DT, 1>(a, st);
-  if (a.M <= 32) return run_skinny<DT, 2>(a, st);
-  if (a.M <= 64) return run_skinny<DT, 4>(a, st);
-  const size_t b = DT == 2 ? 4 : 2;
-  const bool vec = a.n % 4 == 0 && a.ld_out % 4 == 0 && (uintptr_t)a.out % (4 * b) == 0;
-  return vec ? run_tiles<DT, true>(a, st) : run_tiles<DT, false>(a, st);
+  const double u = (double)cdiv64(a.k, 128);
+  auto rounds = [&](int tm, int tn) { return (double)cdiv64(cdiv64(a.M, tm) * cdiv64(a.n, tn), 256); };
+  const double stream = 3.0 + (double)a.n * a.k / 5.2e6;
+  const double t32 = std::max(1.8 + rounds(32, 32) * (0.4 + 0.1 * u), stream);
+  if (a.M <= 32 && std::max(3.8, stream - 0.1) <= t32) return a.M <= 16 ? run_skinny<DT, 1>(a, st) : run_skinny<DT, 2>(a, st);
+  const double t64 = rounds(64, 64) * (4.6 + 0.19 * u), t128 = 1.0 + rounds(128, 128) * (4.4 + 0.55 * u);
+  const double t256 = rounds(256, 256) * (14.0 + 1.25 * u), best = std::min({t32, t64, t128, t256});
+  if (best == t32) return launch_split<DT, 2, 2, 2>(a, 32, 4, st);
+  if (best == t64) return launch_split<DT, 4, 4, 2>(a, 64, 4, st);
+  return best == t128 ? run_tile<DT, 128, 128>(a, st) : run_tile<DT, 256, 256>(a, st);
 }
 
 template <int DT>
 int raise_lds() {
   const void* f[] = {(const void*)linear_tile<DT, 256, 256, true>, (const void*)linear_tile<DT, 256, 256, false>,
-                     (const void*)linear_tile<DT, 128, 128, true>,
-                     (const void*)linear_tile<DT, 128, 128, false>, (const void*)linear_skinny<DT, 1, 5>,
-                     (const void*)linear_skinny<DT, 1, 3>,         (const void*)linear_skinny<DT, 2, 3>,
-                     (const void*)linear_skinny<DT, 2, 2>,         (const void*)linear_skinny<DT, 4, 2>};
+                     (const void*)linear_tile<DT, 128, 128, true>, (const void*)linear_tile<DT, 128, 128, false>,
+                     (const void*)linear_split<DT, 1, 1, 5>,       (const void*)linear_split<DT, 1, 1, 3>,
+                     (const void*)linear_split<DT, 2, 1, 3>,       (const void*)linear_split<DT, 2, 1, 2>,
+                     (const void*)linear_split<DT, 2, 2, 2>,       (const void*)linear_split<DT, 4, 4, 2>};
   for (const void* k : f) {
     const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != hipSuccess) return (int)e;

@@ -326,7 +326,9 @@ def test_rows_are_independent(H):
 LIN = [  # n, k, m
     (1, 1, 1), (3, 5, 2), (16, 16, 1), (17, 63, 16), (15, 64, 17), (64, 65, 64), (100, 1000, 65), (777, 1000, 300),
     (2560, 10240, 1), (10240, 2560, 1), (2560, 10240, 32), (2560, 2560, 5), (320, 10240, 33), (513, 129, 129),
-    (1024, 512, 1023), (2500, 640, 513), (4, 131071, 3), (333, 4096, 257), (2560, 320, 2048), (4096, 1040, 1100)]
+    (1024, 512, 1023), (2500, 640, 513), (4, 131071, 3), (333, 4096, 257), (2560, 320, 2048), (4096, 1040, 1100),
+    # few stages of K in many tiles, so that a workgroup's loads run far ahead
+    (8200, 40, 8200), (5000, 100, 3000), (4100, 64, 1300), (2600, 130, 1700), (300, 8, 700), (8192, 200, 600)]
 
 
 def linear_inputs(g, n, k, m, dt, bias=True, extreme=False):
