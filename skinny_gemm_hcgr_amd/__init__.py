@@ -674,7 +674,11 @@ class _Op:
         self.handle = create(cfg, self.device)
         self.dtype = torch_dtype(cfg.dtype)
         self._torch = torch
+        self._f32, self._i8 = torch.float32, torch.int8
         self._lib = load_library()
+        # torch's current stream as a raw hipStream_t, without the stream object where torch offers that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -708,7 +712,7 @@ class _Op:
 
     def _rows8(self, name, t, m, cols):
         """The same for int8 rows, which are read in whole 16-byte pieces."""
-        p, ld = self._rows(name, t, self._torch.int8, m, cols)
+        p, ld = self._rows(name, t, self._i8, m, cols)
         if m == 1:
             ld = _round16(cols)
         if m and cols % 16 and t.untyped_storage().nbytes() < t.storage_offset() + (m - 1) * ld + _round16(cols):
@@ -718,7 +722,7 @@ class _Op:
 
     def _raw(self, stream):
         if stream is None:
-            return self._torch.cuda.current_stream(self.device).cuda_stream
+            return self._current(self.device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _made(self, stream, *tensors):
@@ -738,7 +742,7 @@ class _Op:
 
     def _quantized(self, m, cols):
         """int8 [m, cols] at a pitch of whole 16-byte pieces, and its scales."""
-        return self._empty((m, _round16(cols)), self._torch.int8)[:, :cols], self._empty((m,), self._torch.float32)
+        return self._empty((m, _round16(cols)), self._i8)[:, :cols], self._empty((m,), self._f32)
 
 
 class Block(_Op):
@@ -751,7 +755,7 @@ class Block(_Op):
 
     def alloc_norm(self, M: int, *, quantize: bool = False, keep: bool = False) -> dict:
         """``quantize``: q and q_scale in place of x; ``keep``: x as well."""
-        f32, hs = self._torch.float32, self.cfg.hs
+        f32, hs = self._f32, self.cfg.hs
         out = {"rrms": self._empty((M,), f32)}
         if quantize:
             out["q"], out["q_scale"] = self._quantized(M, hs)
@@ -760,17 +764,17 @@ class Block(_Op):
         return out
 
     def alloc_norm_bwd(self, M: int) -> dict:
-        return {"dx": self._empty((M, self.cfg.hs), self.dtype), "dw": self._empty((self.cfg.hs,), self._torch.float32)}
+        return {"dx": self._empty((M, self.cfg.hs), self.dtype), "dw": self._empty((self.cfg.hs,), self._f32)}
 
     def alloc_residual(self, M: int, *, norm: bool = True, quantize: bool = False, keep: bool = False) -> dict:
         """``norm``: the next norm is wanted (w_pre is given)."""
         out = self.alloc_norm(M, quantize=quantize, keep=keep) if norm else {}
-        out["rrms"] = self._empty((M, 2), self._torch.float32)
+        out["rrms"] = self._empty((M, 2), self._f32)
         out["R2"] = self._empty((M, self.cfg.k), self.dtype)
         return out
 
     def alloc_residual_bwd(self, M: int, *, gates: bool = True, post: bool = True, pre: bool = True) -> dict:
-        c, f32 = self.cfg, self._torch.float32
+        c, f32 = self.cfg, self._f32
         out = {"dR": self._empty((M, c.k), self.dtype), "dy": self._empty((M, c.hs), self.dtype)}
         if gates:
             out["dinj"] = self._empty((M, c.hc), self.dtype)
@@ -785,7 +789,7 @@ class Block(_Op):
         return self._empty((hcgr_block_workspace_size(self.handle, M),), self._torch.uint8)
 
     def _norm_outputs(self, out, M):
-        hs, f32 = self.cfg.hs, self._torch.float32
+        hs, f32 = self.cfg.hs, self._f32
         x = self._dense("x", out.get("x"), self.dtype, (M, hs))
         q, ld_q, qs = out.get("q"), 0, None
         if q is not None:
@@ -811,12 +815,12 @@ class Block(_Op):
         xn, q, ld_q, qs = self._norm_outputs(out, M)
         _check(self._lib.hcgr_block_norm(
             self.handle, px, ld_x, self._dense("w", w, self.dtype, (hs,)), M, xn, q, ld_q, qs,
-            self._dense("rrms", out.get("rrms"), self._torch.float32, (M,)), self._raw(stream)), "hcgr_block_norm")
+            self._dense("rrms", out.get("rrms"), self._f32, (M,)), self._raw(stream)), "hcgr_block_norm")
         return out
 
     def norm_bwd(self, x, w, rrms, dxn, *, out: dict | None = None, workspace=None, stream=None) -> dict:
         """Gradients dx [M, HS] and dw [HS] (float32, summed over the tokens) of ``norm``."""
-        M, hs, f32 = x.shape[0], self.cfg.hs, self._torch.float32
+        M, hs, f32 = x.shape[0], self.cfg.hs, self._f32
         px, ld_x = self._rows("x", x, self.dtype, M, hs)
         if out is None:
             out = self.alloc_norm_bwd(M)
@@ -847,7 +851,7 @@ class Block(_Op):
             self.handle, self._dense("R", R, dt, (M, k)), py, ld_y, pi, ld_i,
             self._dense("w_post", w_post, dt, (hs,)), self._dense("w_pre", w_pre, dt, (hs,)), M,
             self._dense("R2", out["R2"], dt, (M, k)), x, q, ld_q, qs,
-            self._dense("rrms", out.get("rrms"), self._torch.float32, (M, 2)), self._raw(stream)),
+            self._dense("rrms", out.get("rrms"), self._f32, (M, 2)), self._raw(stream)),
             "hcgr_block_residual")
         return out
 
@@ -855,7 +859,7 @@ class Block(_Op):
                      stream=None) -> dict:
         """Gradients dR, dy, dinj, dw_post and dw_pre (those whose input is
         given) of ``residual`` from dR2 [M, HC*HS] and dx [M, HS]."""
-        c, dt, f32 = self.cfg, self.dtype, self._torch.float32
+        c, dt, f32 = self.cfg, self.dtype, self._f32
         M, hs, k = R.shape[0], c.hs, c.hc * c.hs
         py, ld_y = self._rows("y", y, dt, M, hs)
         pi, ld_i = self._rows("inj", inj, dt, M, c.hc) if inj is not None else (None, 0)
@@ -903,13 +907,13 @@ class Int8Linear(_Op):
             self._made(stream, *out)
         q, ld_q = self._rows8("q", out[0], M, k)
         _check(self._lib.hcgr_linear_quantize(
-            self.handle, px, ld_x, M, q, ld_q, self._dense("q_scale", out[1], self._torch.float32, (M,)),
+            self.handle, px, ld_x, M, q, ld_q, self._dense("q_scale", out[1], self._f32, (M,)),
             self._raw(stream)), "hcgr_linear_quantize")
         return out
 
     def forward(self, q, q_scale, w, w_scale, bias=None, *, out=None, stream=None):
         """out [M, N] from tokens q int8 [M, K] and weights w int8 [N, K]."""
-        c, f32, M = self.cfg, self._torch.float32, q.shape[0]
+        c, f32, M = self.cfg, self._f32, q.shape[0]
         pq, ld_q = self._rows8("q", q, M, c.k)
         pw, ld_w = self._rows8("w", w, c.n, c.k)
         if out is None:
