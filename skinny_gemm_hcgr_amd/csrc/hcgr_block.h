@@ -19,6 +19,7 @@ struct NormArgs {
   int64_t ld_q;
   float *q_scale, *rr_post, *rr_pre;  // rr_*: column of each norm, NULL when not wanted
   int rr_ld;                          // floats from one token's r to the next
+  int nt = 0;                         // set by the launch: outputs with the streaming policy
 };
 
 // Backward of both. For hcgr_block_norm_bwd: residual = false, R = x, w_pre =
@@ -39,6 +40,7 @@ int launch_norm(const NormArgs& a, int dtype, bool residual, void* stream);
 int launch_norm_bwd(const NormBwdArgs& a, int dtype, bool residual, void* stream);
 // Rows -> int8 rows and a scale each: launch_norm without the norm.
 int launch_quantize(const NormArgs& a, int dtype, void* stream);
+int configure_block_kernels();
 size_t norm_bwd_workspace(int hs, int64_t M);
 
 struct LinearArgs {

@@ -316,7 +316,7 @@ __global__ __launch_bounds__(1024) void norm_loop(NormArgs a) {
 // dy and sums the weight gradients of its columns; norm_bwd_sum adds the
 // groups' sums in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int kRowGroups = 512;  // partial sums of the weight gradients
+constexpr int kRowGroups = 768;  // partial sums of the weight gradients
 constexpr int kColThreads = 256;
 
 // Workspace: m_pre and m_post of each row, then [groups][2][HS] partial sums.
@@ -513,6 +513,10 @@ template <typename S>
 __device__ __forceinline__ rsrc_t row_of(const void* base, int64_t off, uint32_t bytes) {
   return base ? make_rsrc(reinterpret_cast<const S*>(base) + off, bytes) : make_rsrc(nullptr, 0u);
 }
+template <typename S>
+__device__ __forceinline__ i32x4_t words_of(const void* base, int64_t off, uint32_t bytes) {
+  return range_words(reinterpret_cast<const S*>(base) + (base ? off : 0), base ? bytes : 0u);
+}
 __device__ __forceinline__ uint32_t piece_at(int j, uint32_t row) {
   const uint32_t at = (threadIdx.x + (uint32_t)j * blockDim.x) * 16u;
   return at < row ? at : 0x7ffffff0u;
@@ -524,14 +528,17 @@ __device__ __forceinline__ uint4 piece(rsrc_t r, uint32_t at, uint32_t stream = 
 // store whose scalar offset is a register, the compiler lets the next
 // instruction overwrite the stored registers, and on MI355X such stores have
 // written the new values (with a constant scalar offset it keeps them apart).
+// nt: the streaming policy, for outputs too large for the caches to keep until
+// they are read.
 template <typename T>
-__device__ __forceinline__ void put(rsrc_t r, uint32_t at, uint32_t stream, const float (&f)[vec<T>()]) {
+__device__ __forceinline__ void put(rsrc_t r, uint32_t at, uint32_t stream, const float (&f)[vec<T>()], int nt) {
   typename T::S s[vec<T>()];
 #pragma unroll
   for (int i = 0; i < vec<T>(); ++i) s[i] = down<T>(f[i]);
   u32x4_t u;
   __builtin_memcpy(&u, s, 16);
-  __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)(at + stream), 0, 0);
+  if (nt) __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)(at + stream), 0, kNonTemporal);
+  else __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)(at + stream), 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -606,7 +613,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
           r[i] = fmaf(iw[s], z[i], a.rho * r[i]);
           u[j][i] += r[i];
         }
-        put<T>(r2, at, s * row, r);
+        put<T>(r2, at, s * row, r, a.nt);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) u[j][i] *= 1.0f / (float)HC;
@@ -639,7 +646,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
     for (int i = 0; i < V; ++i) u[j][i] *= ru;
   if (NORM && a.x) {
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) put<T>(row_of<S>(a.x, m * hs, row), piece_at(j, row), 0, u[j]);
+    for (int j = 0; j < NCH; ++j) put<T>(row_of<S>(a.x, m * hs, row), piece_at(j, row), 0, u[j], a.nt);
   }
   if (a.q) {
     uint32_t am = 0;
@@ -662,14 +669,34 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
 // workgroup, in one pass over the data. A workgroup walks every G-th row,
 // keeps the weights and the sums of its columns' weight gradients in
 // registers, and gets all row sums from one reduction (see above norm_bwd_rows).
-// One-wave rows: four rows at a time, the four waves' sums meet in LDS.
+// One-wave rows: four rows at a time, the four waves' sums meet in LDS. Up to
+// 512 threads the next row's pieces come to LDS behind this row's products and
+// stores, each wave's into a place of its own (no barrier). At M = 8192, HC =
+// 4, HS = 2560 the pass takes 158 us (4.0 TB/s; 5.2 TB/s, what a copy reaches,
+// would take 121): 194 us with the loads of a row waiting for the row before,
+// 169 with the next row ahead, 162 with three workgroups a CU (128 registers)
+// in place of two, the rest by streaming stores.
 // ---------------------------------------------------------------------------
+constexpr int bwd_loads(int hc) { return hc ? 2 * hc + 2 : 2; }  // hc = 0: the norm alone
+// Dynamic LDS of norm_bwd_row: the waves' places, and room for the sums of
+// one-wave rows (three waves' two gradients).
+inline size_t bwd_lds(int hc, int nch, int waves, int v, bool ahead, bool one_wave) {
+  const size_t ring = ahead ? (size_t)waves * bwd_loads(hc) * nch * 1024 : 0;
+  const size_t sums = one_wave ? (size_t)3 * 2 * 64 * nch * v * 4 : 0;
+  return ring > sums ? ring : sums;
+}
+
 template <typename T, int HC, int NCH, int THREADS, bool RES>
-__global__ __launch_bounds__(THREADS) void norm_bwd_row(NormBwdArgs a) {
+__global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void norm_bwd_row(NormBwdArgs a) {
   using S = typename T::S;
   constexpr int V = vec<T>(), N = RES ? HC + 3 : 1;
+  constexpr bool AHEAD = THREADS <= 512;
+  constexpr int L = bwd_loads(RES ? HC : 0) * NCH;  // a wave's loads a row, 1 KB each
   __shared__ float red[2][16 * N];
-  __shared__ float wred[3][2][64 * NCH * V];  // one-wave rows only
+  extern __shared__ uint8_t ring[];  // [waves][L KB]; at the end the sums of one-wave rows
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.y * blockDim.x + threadIdx.x) / 64), lane = (int)threadIdx.x % 64;
+  const uint8_t* mine = ring + wave * (L * 1024) + lane * 16;
+  const uint32_t mine0 = (uint32_t)(uintptr_t)(lds_u8_t*)ring + (uint32_t)(wave * (L * 1024));
   const int hs = a.hs;
   const bool wpre = a.w_pre != nullptr, wpost = RES && a.w_post != nullptr;
   const uint32_t row = (uint32_t)hs * sizeof(S);  // bytes of a stream
@@ -682,31 +709,93 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_row(NormBwdArgs a) {
   }
   int flip = 0;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
-  for (int64_t m = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y); m < a.M;
-       m += stride) {
-    // an absent tensor is an empty range, which reads as zero
-    const rsrc_t rR = row_of<S>(a.R, m * a.ld_R, HC * row), rD = row_of<S>(a.dR2, m * a.ld_R, HC * row);
-    const rsrc_t rY = row_of<S>(a.y, m * a.ld_y, row), rX = row_of<S>(a.dx, m * hs, row);
-    uint4 rr[NCH][HC], dr[NCH][HC], yr[NCH], xr[NCH];
+  uint4 rr[NCH][HC], dr[NCH][HC], yr[NCH], xr[NCH];
+  // Row m's pieces to LDS (AHEAD) or registers. An absent tensor, and a row
+  // past the last, is an empty range, which reads as zero.
+  auto fetch = [&](int64_t m) {
+    const bool in = m < a.M;
+    const void* R = in && wpre ? a.R : nullptr;
+    if constexpr (AHEAD) {
+      const i32x4_t rR = words_of<S>(R, m * a.ld_R, HC * row), rX = words_of<S>(in ? a.dx : nullptr, m * hs, row);
+      const i32x4_t rD = words_of<S>(RES && in ? a.dR2 : nullptr, m * a.ld_R, HC * row);
+      const i32x4_t rY = words_of<S>(RES && in ? a.y : nullptr, m * a.ld_y, row);
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const uint32_t at = piece_at(j, row);
-      if constexpr (RES) yr[j] = piece(rY, at);
-      if (wpre) {
+      for (int j = 0; j < NCH; ++j) {
+        const uint32_t at = piece_at(j, row), to = mine0 + (uint32_t)(j * (L / NCH) * 1024);
+        load_lds(rX, at, to);
+#pragma unroll
+        for (int s = 0; s < HC; ++s) load_lds(rR, at + s * row, to + (1 + s) * 1024);
+        if constexpr (RES) {
+          load_lds(rY, at, to + (1 + HC) * 1024);
+#pragma unroll
+          for (int s = 0; s < HC; ++s) load_lds(rD, at + s * row, to + (2 + HC + s) * 1024);
+        }
+      }
+    } else {
+      const rsrc_t rR = row_of<S>(R, m * a.ld_R, HC * row), rX = row_of<S>(in ? a.dx : nullptr, m * hs, row);
+      const rsrc_t rD = row_of<S>(RES && in ? a.dR2 : nullptr, m * a.ld_R, HC * row);
+      const rsrc_t rY = row_of<S>(RES && in ? a.y : nullptr, m * a.ld_y, row);
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const uint32_t at = piece_at(j, row);
         xr[j] = piece(rX, at);
+        yr[j] = piece(rY, at);
 #pragma unroll
         for (int s = 0; s < HC; ++s) rr[j][s] = piece(rR, at, s * row);
-      }
-      if constexpr (RES) {
 #pragma unroll
         for (int s = 0; s < HC; ++s) dr[j][s] = piece(rD, at, s * row);
       }
     }
-    const float ry = wpost ? a.rr_post[m * a.rr_ld] : 1.0f, ru = wpre ? a.rr_pre[m * a.rr_ld] : 1.0f;
+  };
+  // the row's scalars, asked for one row ahead too
+  struct Scalars {
+    float ry, ru;
+    S inj[HC];
+  };
+  auto scalars = [&](int64_t m) {
+    Scalars z;
+    m = m < a.M ? m : a.M - 1;
+    z.ry = wpost ? a.rr_post[m * a.rr_ld] : 1.0f;
+    z.ru = wpre ? a.rr_pre[m * a.rr_ld] : 1.0f;
+    if (RES && a.inj) {
+#pragma unroll
+      for (int s = 0; s < HC; ++s) z.inj[s] = reinterpret_cast<const S*>(a.inj)[m * a.ld_inj + s];
+    }
+    return z;
+  };
+  const int64_t m0 = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y);
+  Scalars sc = scalars(m0);
+  if constexpr (AHEAD) fetch(m0);
+  for (int64_t m = m0; m < a.M; m += stride) {
+    const Scalars now = sc;
+    if constexpr (AHEAD) {
+      // the loads are older than the row before's HC + 1 stores a piece, which
+      // may still be on their way (the norm's one store is optional)
+      if (RES && m != m0) landed<(HC + 1) * NCH>();
+      else landed<0>();
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const uint8_t* from = mine + j * (L / NCH) * 1024;
+        xr[j] = ld16(from);
+#pragma unroll
+        for (int s = 0; s < HC; ++s) rr[j][s] = ld16(from + (1 + s) * 1024);
+        if constexpr (RES) {
+          yr[j] = ld16(from + (1 + HC) * 1024);
+#pragma unroll
+          for (int s = 0; s < HC; ++s) dr[j][s] = ld16(from + (2 + HC + s) * 1024);
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's place is read
+      fetch(m + stride);
+    } else {
+      fetch(m);
+    }
+    sc = scalars(m + stride);
+    const float ry = now.ry, ru = now.ru;
     float iw[HC], iwm = 0.0f;
 #pragma unroll
     for (int s = 0; s < HC; ++s) {
-      iw[s] = RES && a.inj ? gate(up(reinterpret_cast<const S*>(a.inj)[m * a.ld_inj + s]), HC) : 1.0f;
+      iw[s] = RES && a.inj ? gate(up(now.inj[s]), HC) : 1.0f;
       iwm += iw[s] * (1.0f / (float)HC);
     }
     // u, and the row sums B_s, A, C, D
@@ -785,7 +874,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_row(NormBwdArgs a) {
         }
       }
       if constexpr (!RES) {
-        if (a.dR) put<T>(row_of<S>(a.dR, m * hs, row), at, 0, du);
+        if (a.dR) put<T>(row_of<S>(a.dR, m * hs, row), at, 0, du, 1);
       } else {
         float dz[V] = {};
 #pragma unroll
@@ -798,7 +887,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_row(NormBwdArgs a) {
             dz[i] = fmaf(iw[s], d[i], dz[i]);
             d[i] *= a.rho;
           }
-          put<T>(row_of<S>(a.dR, m * a.ld_R, HC * row), at, s * row, d);
+          put<T>(row_of<S>(a.dR, m * a.ld_R, HC * row), at, s * row, d, 1);
         }
         if (wpost) {
           float h[V], g[V];
@@ -811,12 +900,15 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_row(NormBwdArgs a) {
             dz[i] = ry * (dz[i] * (1.0f + g[i]) - h[i] * m_post);
           }
         }
-        put<T>(row_of<S>(a.dy, m * hs, row), at, 0, dz);
+        put<T>(row_of<S>(a.dy, m * hs, row), at, 0, dz, 1);
       }
     }
   }
+  if constexpr (AHEAD) landed<0>();  // no load into this workgroup's LDS outlives it
   if (!a.dw_post && !a.dw_pre) return;
   if (blockDim.y > 1) {  // four waves, blockDim.x = 64
+    float(*wred)[2][64 * NCH * V] = reinterpret_cast<float(*)[2][64 * NCH * V]>(ring);
+    __syncthreads();  // every wave's place is read
     const int w = (int)threadIdx.y, t = (int)threadIdx.x;
     if (w > 0) {
 #pragma unroll
@@ -870,6 +962,15 @@ bool aligned(const NormBwdArgs& a, int b) {
          al16(a.w_pre) && al16(a.dR2) && al16(a.dx) && al16(a.dR) && al16(a.dy);
 }
 
+// Whether outputs of that many rows of HS values a token outgrow the L2s (8 x 4
+// MB). Measured with the streaming policy on one MI355X (HS = 2560, bf16):
+// residual M = 16384 HC = 4 148 -> 142 us, but the residual of 333 tokens, whose
+// outputs stay in the caches, 3.7 -> 4.0 us. (The backward kernels always use
+// it: a choice at run time costs registers that they do not have.)
+bool streamed(int64_t M, int hs, int rows, size_t b) {
+  return (double)M * hs * rows * (double)b > 32.0 * 1024 * 1024;
+}
+
 int loop_threads(int64_t pieces) {
   const int64_t t = cdiv64(pieces, 64) * 64;
   return (int)(t < 1024 ? t : 1024);
@@ -885,7 +986,8 @@ int forward_loop(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
 }
 
 template <typename T, int NCH>
-int forward_row(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
+int forward_row(NormArgs a, bool residual, bool norm, hipStream_t st) {
+  a.nt = streamed(a.M, a.hs, residual ? a.hc + 1 : 1, sizeof(typename T::S));
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   const int nw = (int)cdiv64(pieces, 64 * NCH);
   const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1), grid((unsigned)cdiv64(a.M, blk.y));
@@ -932,12 +1034,23 @@ int backward_row(const NormBwdArgs& a, bool residual, hipStream_t st) {
   const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1);
   const int64_t groups = bwd_groups(cdiv64(a.M, blk.y));
   const dim3 grid((unsigned)groups);
-  if (!residual) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, false>), grid, blk, 0, st, a);
-  else if (a.hc == 1) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, true>), grid, blk, 0, st, a);
-  else if (a.hc == 2) hipLaunchKernelGGL((norm_bwd_row<T, 2, NCH, THREADS, true>), grid, blk, 0, st, a);
-  else if (a.hc == 4) hipLaunchKernelGGL((norm_bwd_row<T, 4, NCH, THREADS, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((norm_bwd_row<T, 8, NCH, THREADS, true>), grid, blk, 0, st, a);
+  const size_t lds = bwd_lds(residual ? a.hc : 0, NCH, (int)(blk.x * blk.y / 64), vec<T>(), THREADS <= 512, nw == 1);
+  if (!residual) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, false>), grid, blk, lds, st, a);
+  else if (a.hc == 1) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, true>), grid, blk, lds, st, a);
+  else if (a.hc == 2) hipLaunchKernelGGL((norm_bwd_row<T, 2, NCH, THREADS, true>), grid, blk, lds, st, a);
+  else if (a.hc == 4) hipLaunchKernelGGL((norm_bwd_row<T, 4, NCH, THREADS, true>), grid, blk, lds, st, a);
+  else hipLaunchKernelGGL((norm_bwd_row<T, 8, NCH, THREADS, true>), grid, blk, lds, st, a);
   return sum_groups(a, groups, st);
+}
+
+template <typename T>
+hipError_t raise_lds() {
+  const void* f[] = {(const void*)norm_bwd_row<T, 4, 1, 512, true>, (const void*)norm_bwd_row<T, 8, 1, 512, true>};
+  for (const void* k : f) {
+    const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, 152 * 1024);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T>
@@ -971,6 +1084,13 @@ int launch_norm_bwd(const NormBwdArgs& a, int dtype, bool residual, void* stream
   return dtype == 0 ? backward_of<Bf16>(a, residual, st)
          : dtype == 1 ? backward_of<Fp16>(a, residual, st)
                       : backward_of<Fp32>(a, residual, st);
+}
+
+// Raises the dynamic-LDS limit of the backward kernels on the current device.
+int configure_block_kernels() {
+  for (const hipError_t e : {raise_lds<Bf16>(), raise_lds<Fp16>(), raise_lds<Fp32>()})
+    if (e != hipSuccess) return (int)e;
+  return (int)hipSuccess;
 }
 
 size_t norm_bwd_workspace(int hs, int64_t M) {

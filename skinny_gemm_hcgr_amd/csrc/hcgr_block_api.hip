@@ -280,6 +280,20 @@ hcgr_status on_device(int device, void* stream, F launch) {
   return ok();
 }
 
+// Sets the kernels' attributes on `device`.
+hcgr_status configure(int device, int (*set)()) {
+  int cur = -1;
+  hipError_t e = hipGetDevice(&cur);
+  if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
+  if (cur != device && (e = hipSetDevice(device)) != hipSuccess)
+    return fail(HCGR_ERR_HIP, "hipSetDevice: %s", hipGetErrorString(e));
+  const int ke = set();
+  restore_device(device, cur);
+  if (ke != (int)hipSuccess)
+    return fail(HCGR_ERR_HIP, "kernel attribute set-up failed: %s", hipGetErrorString((hipError_t)ke));
+  return HCGR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -290,6 +304,7 @@ hcgr_status hcgr_block_create(const hcgr_block_config* cfg, int device, hcgr_blo
   hcgr_status st = check_block(cfg);
   if (st != HCGR_OK) return st;
   if ((st = check_device(device)) != HCGR_OK) return st;
+  if ((st = configure(device, hcgr::configure_block_kernels)) != HCGR_OK) return st;
   hcgr_block_op* op = new (std::nothrow) hcgr_block_op;
   if (!op) return fail(HCGR_ERR_INVALID_ARGUMENT, "out of host memory");
   op->cfg = *cfg;
@@ -431,15 +446,7 @@ hcgr_status hcgr_linear_create(const hcgr_linear_config* cfg, int device, hcgr_l
   hcgr_status st = check_linear(cfg);
   if (st != HCGR_OK) return st;
   if ((st = check_device(device)) != HCGR_OK) return st;
-  int cur = -1;
-  hipError_t e = hipGetDevice(&cur);
-  if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
-  if (cur != device && (e = hipSetDevice(device)) != hipSuccess)
-    return fail(HCGR_ERR_HIP, "hipSetDevice: %s", hipGetErrorString(e));
-  const int ke = hcgr::configure_linear_kernels();
-  restore_device(device, cur);
-  if (ke != (int)hipSuccess)
-    return fail(HCGR_ERR_HIP, "kernel attribute set-up failed: %s", hipGetErrorString((hipError_t)ke));
+  if ((st = configure(device, hcgr::configure_linear_kernels)) != HCGR_OK) return st;
   hcgr_linear_op* op = new (std::nothrow) hcgr_linear_op;
   if (!op) return fail(HCGR_ERR_INVALID_ARGUMENT, "out of host memory");
   op->cfg = *cfg;

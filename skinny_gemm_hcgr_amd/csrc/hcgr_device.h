@@ -96,4 +96,33 @@ __device__ __forceinline__ void lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)\
 // logistic function through the hardware 2^x and reciprocal: 1/(1 + 2^(-v*log2 e))
 __device__ __forceinline__ float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+// The four words of make_rsrc's descriptor.
+__device__ __forceinline__ i32x4_t range_words(const void* base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)p), __builtin_amdgcn_readfirstlane((int)(p >> 32) & 0xffff),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// 1 KB from memory to LDS at `lds` (lane l's 16 bytes at lds + 16*l). Written
+// as assembly so that the compiler does not make every LDS read wait for all
+// loads in flight: the kernel waits itself (landed). It writes no register but
+// m0, which nothing else in these kernels uses; m0 needs one wait state before
+// such a load.
+__device__ __forceinline__ void load_lds(i32x4_t r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(r), "s"(lds)
+               : "memory");
+}
+// The same, four bytes a lane (256 bytes).
+__device__ __forceinline__ void load_lds4(i32x4_t r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(r), "s"(lds)
+               : "memory");
+}
+// Until at most N of this wave's vector memory operations are outstanding.
+template <int N>
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
+
 }  // namespace hcgr
