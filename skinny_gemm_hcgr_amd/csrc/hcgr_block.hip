@@ -521,24 +521,52 @@ __device__ __forceinline__ uint32_t piece_at(int j, uint32_t row) {
   const uint32_t at = (threadIdx.x + (uint32_t)j * blockDim.x) * 16u;
   return at < row ? at : 0x7ffffff0u;
 }
-__device__ __forceinline__ uint4 piece(rsrc_t r, uint32_t at, uint32_t stream = 0) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, (int)stream, 0));
-}
-// The stream's offset goes into the vector offset here: after a 16-byte buffer
-// store whose scalar offset is a register, the compiler lets the next
-// instruction overwrite the stored registers, and on MI355X such stores have
-// written the new values (with a constant scalar offset it keeps them apart).
+// A token's row of one or several streams. AL: as above; otherwise the row
+// starts at any element and its pieces go by pointers.
+template <typename T, bool AL>
+struct Row {
+  using S = typename T::S;
+  rsrc_t r;
+  S* p;
+  int hs;
+  __device__ __forceinline__ Row(const void* base, int64_t off, int streams, int hs_) {
+    hs = hs_;
+    if constexpr (AL) r = row_of<S>(base, off, (uint32_t)(streams * hs * (int)sizeof(S)));
+    else p = base ? const_cast<S*>(reinterpret_cast<const S*>(base)) + off : nullptr;
+  }
+  // piece j of this thread in stream s
+  __device__ __forceinline__ uint4 get(int j, int s = 0) const {
+    if constexpr (AL) {
+      const uint32_t row = (uint32_t)hs * sizeof(S);
+      return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)piece_at(j, row), (int)(s * row), 0));
+    } else {
+      const int c = ((int)threadIdx.x + j * (int)blockDim.x) * vec<T>();
+      return p ? load_raw<T, false>(p + (int64_t)s * hs + c, hs - c) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void put(int j, int s, const float (&f)[vec<T>()], int nt) const;
+};
 // nt: the streaming policy, for outputs too large for the caches to keep until
-// they are read.
-template <typename T>
-__device__ __forceinline__ void put(rsrc_t r, uint32_t at, uint32_t stream, const float (&f)[vec<T>()], int nt) {
-  typename T::S s[vec<T>()];
+// they are read. The stream's offset goes into the vector offset here: after a
+// 16-byte buffer store whose scalar offset is a register, the compiler lets
+// the next instruction overwrite the stored registers, and on MI355X such
+// stores have written the new values (with a constant scalar offset it keeps
+// them apart).
+template <typename T, bool AL>
+__device__ __forceinline__ void Row<T, AL>::put(int j, int s, const float (&f)[vec<T>()], int nt) const {
+  if constexpr (AL) {
+    typename T::S v[vec<T>()];
 #pragma unroll
-  for (int i = 0; i < vec<T>(); ++i) s[i] = down<T>(f[i]);
-  u32x4_t u;
-  __builtin_memcpy(&u, s, 16);
-  if (nt) __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)(at + stream), 0, kNonTemporal);
-  else __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)(at + stream), 0, 0);
+    for (int i = 0; i < vec<T>(); ++i) v[i] = down<T>(f[i]);
+    u32x4_t u;
+    __builtin_memcpy(&u, v, 16);
+    const uint32_t row = (uint32_t)hs * sizeof(S), at = piece_at(j, row) + s * row;
+    if (nt) __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)at, 0, kNonTemporal);
+    else __builtin_amdgcn_raw_buffer_store_b128(u, r, (int)at, 0, 0);
+  } else {
+    const int c = ((int)threadIdx.x + j * (int)blockDim.x) * vec<T>();
+    store<T, false>(p + (int64_t)s * hs + c, hs - c, f);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -548,7 +576,7 @@ __device__ __forceinline__ void put(rsrc_t r, uint32_t at, uint32_t stream, cons
 // 64 * NCH pieces take one wave, four rows a workgroup, without barriers;
 // wider rows take the whole workgroup.
 // ---------------------------------------------------------------------------
-template <typename T, int HC, int NCH, bool RES, bool NORM>
+template <typename T, int HC, int NCH, bool AL, bool RES, bool NORM>
 __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
   using S = typename T::S;
   constexpr int V = vec<T>();
@@ -558,18 +586,15 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
   const int64_t m = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y);
   if (m >= a.M) return;  // blockDim.y > 1 only without barriers
   const bool wpre = a.w_pre != nullptr, wpost = RES && a.w_post != nullptr;
-  const uint32_t row = (uint32_t)hs * sizeof(S);  // bytes of a stream
-  const rsrc_t rR = row_of<S>(a.R, m * a.ld_R, HC * row), rY = row_of<S>(a.y, m * a.ld_y, row);
-  const rsrc_t rG = row_of<S>(a.w_post, 0, row), rW = row_of<S>(a.w_pre, 0, row);
+  const Row<T, AL> rR(a.R, m * a.ld_R, HC, hs), rY(a.y, m * a.ld_y, 1, hs), rG(a.w_post, 0, 1, hs), rW(a.w_pre, 0, 1, hs);
   uint4 rr[NCH][HC], yr[NCH], gr[NCH], wr[NCH];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    const uint32_t at = piece_at(j, row);
-    if constexpr (RES) yr[j] = piece(rY, at);
+    if constexpr (RES) yr[j] = rY.get(j);
 #pragma unroll
-    for (int s = 0; s < HC; ++s) rr[j][s] = piece(rR, at, s * row);
-    if (wpost) gr[j] = piece(rG, at);
-    if (NORM && wpre) wr[j] = piece(rW, at);
+    for (int s = 0; s < HC; ++s) rr[j][s] = rR.get(j, s);
+    if (wpost) gr[j] = rG.get(j);
+    if (NORM && wpre) wr[j] = rW.get(j);
   }
   float u[NCH][V];
   if constexpr (RES) {
@@ -591,10 +616,9 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
       ry = rrms_of(ss[0], hs, a.eps);
       if (a.rr_post && threadIdx.x == 0) a.rr_post[m * a.rr_ld] = ry;
     }
-    const rsrc_t r2 = row_of<S>(a.R2, m * a.ld_R, HC * row);
+    const Row<T, AL> r2(a.R2, m * a.ld_R, HC, hs);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const uint32_t at = piece_at(j, row);
       float z[V], w[V];
       unpack<T>(yr[j], z);
       if (wpost) {
@@ -613,7 +637,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
           r[i] = fmaf(iw[s], z[i], a.rho * r[i]);
           u[j][i] += r[i];
         }
-        put<T>(r2, at, s * row, r, a.nt);
+        r2.put(j, s, r, a.nt);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) u[j][i] *= 1.0f / (float)HC;
@@ -646,7 +670,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
     for (int i = 0; i < V; ++i) u[j][i] *= ru;
   if (NORM && a.x) {
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) put<T>(row_of<S>(a.x, m * hs, row), piece_at(j, row), 0, u[j], a.nt);
+    for (int j = 0; j < NCH; ++j) Row<T, AL>(a.x, m * hs, 1, hs).put(j, 0, u[j], a.nt);
   }
   if (a.q) {
     uint32_t am = 0;
@@ -659,7 +683,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
-      store_q<V, true>(a.q + m * a.ld_q + c, hs - c, u[j], z);
+      store_q<V, AL>(a.q + m * a.ld_q + c, hs - c, u[j], z);
     }
   }
 }
@@ -686,11 +710,11 @@ inline size_t bwd_lds(int hc, int nch, int waves, int v, bool ahead, bool one_wa
   return ring > sums ? ring : sums;
 }
 
-template <typename T, int HC, int NCH, int THREADS, bool RES>
-__global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void norm_bwd_row(NormBwdArgs a) {
+template <typename T, int HC, int NCH, int THREADS, bool AL, bool RES>
+__global__ __launch_bounds__(THREADS, AL && THREADS <= 512 && NCH == 1 && HC <= 4 ? 4 : 1) void norm_bwd_row(NormBwdArgs a) {
   using S = typename T::S;
   constexpr int V = vec<T>(), N = RES ? HC + 3 : 1;
-  constexpr bool AHEAD = THREADS <= 512;
+  constexpr bool AHEAD = AL && THREADS <= 512 && NCH == 1;
   constexpr int L = bwd_loads(RES ? HC : 0) * NCH;  // a wave's loads a row, 1 KB each
   __shared__ float red[2][16 * N];
   extern __shared__ uint8_t ring[];  // [waves][L KB]; at the end the sums of one-wave rows
@@ -704,8 +728,8 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void no
   uint4 gr[NCH], wr[NCH];
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    gr[j] = piece(row_of<S>(a.w_post, 0, row), piece_at(j, row));
-    wr[j] = piece(row_of<S>(a.w_pre, 0, row), piece_at(j, row));
+    gr[j] = Row<T, AL>(a.w_post, 0, 1, hs).get(j);
+    wr[j] = Row<T, AL>(a.w_pre, 0, 1, hs).get(j);
   }
   int flip = 0;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
@@ -732,18 +756,16 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void no
         }
       }
     } else {
-      const rsrc_t rR = row_of<S>(R, m * a.ld_R, HC * row), rX = row_of<S>(in ? a.dx : nullptr, m * hs, row);
-      const rsrc_t rD = row_of<S>(RES && in ? a.dR2 : nullptr, m * a.ld_R, HC * row);
-      const rsrc_t rY = row_of<S>(RES && in ? a.y : nullptr, m * a.ld_y, row);
+      const Row<T, AL> rR(R, m * a.ld_R, HC, hs), rX(in ? a.dx : nullptr, m * hs, 1, hs);
+      const Row<T, AL> rD(RES && in ? a.dR2 : nullptr, m * a.ld_R, HC, hs), rY(RES && in ? a.y : nullptr, m * a.ld_y, 1, hs);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
-        const uint32_t at = piece_at(j, row);
-        xr[j] = piece(rX, at);
-        yr[j] = piece(rY, at);
+        xr[j] = rX.get(j);
+        yr[j] = rY.get(j);
 #pragma unroll
-        for (int s = 0; s < HC; ++s) rr[j][s] = piece(rR, at, s * row);
+        for (int s = 0; s < HC; ++s) rr[j][s] = rR.get(j, s);
 #pragma unroll
-        for (int s = 0; s < HC; ++s) dr[j][s] = piece(rD, at, s * row);
+        for (int s = 0; s < HC; ++s) dr[j][s] = rD.get(j, s);
       }
     }
   };
@@ -860,7 +882,6 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void no
     }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const uint32_t at = piece_at(j, row);
       float du[V] = {};
       if (wpre) {
         float dx[V], w[V];
@@ -874,7 +895,7 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void no
         }
       }
       if constexpr (!RES) {
-        if (a.dR) put<T>(row_of<S>(a.dR, m * hs, row), at, 0, du, 1);
+        if (a.dR) Row<T, AL>(a.dR, m * hs, 1, hs).put(j, 0, du, 1);
       } else {
         float dz[V] = {};
 #pragma unroll
@@ -887,7 +908,7 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void no
             dz[i] = fmaf(iw[s], d[i], dz[i]);
             d[i] *= a.rho;
           }
-          put<T>(row_of<S>(a.dR, m * a.ld_R, HC * row), at, s * row, d, 1);
+          Row<T, AL>(a.dR, m * a.ld_R, HC, hs).put(j, s, d, 1);
         }
         if (wpost) {
           float h[V], g[V];
@@ -900,7 +921,7 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void no
             dz[i] = ry * (dz[i] * (1.0f + g[i]) - h[i] * m_post);
           }
         }
-        put<T>(row_of<S>(a.dy, m * hs, row), at, 0, dz, 1);
+        Row<T, AL>(a.dy, m * hs, 1, hs).put(j, 0, dz, 1);
       }
     }
   }
@@ -936,12 +957,21 @@ __global__ __launch_bounds__(THREADS, THREADS <= 512 && HC <= 4 ? 4 : 1) void no
   for (int j = 0; j < NCH; ++j) {
     const int c = ((int)threadIdx.x + j * (int)blockDim.x) * V;
     if (c >= hs) continue;
+    if constexpr (AL) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      if (a.dw_post)
-        *reinterpret_cast<float4*>(part + c + i) = make_float4(apost[j][i], apost[j][i + 1], apost[j][i + 2], apost[j][i + 3]);
-      if (a.dw_pre)
-        *reinterpret_cast<float4*>(part + hs + c + i) = make_float4(apre[j][i], apre[j][i + 1], apre[j][i + 2], apre[j][i + 3]);
+      for (int i = 0; i < V; i += 4) {
+        if (a.dw_post)
+          *reinterpret_cast<float4*>(part + c + i) = make_float4(apost[j][i], apost[j][i + 1], apost[j][i + 2], apost[j][i + 3]);
+        if (a.dw_pre)
+          *reinterpret_cast<float4*>(part + hs + c + i) = make_float4(apre[j][i], apre[j][i + 1], apre[j][i + 2], apre[j][i + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (c + i >= hs) break;
+        if (a.dw_post) part[c + i] = apost[j][i];
+        if (a.dw_pre) part[hs + c + i] = apre[j][i];
+      }
     }
   }
 }
@@ -985,18 +1015,18 @@ int forward_loop(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
   return (int)hipGetLastError();
 }
 
-template <typename T, int NCH>
+template <typename T, int NCH, bool AL>
 int forward_row(NormArgs a, bool residual, bool norm, hipStream_t st) {
   a.nt = streamed(a.M, a.hs, residual ? a.hc + 1 : 1, sizeof(typename T::S));
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   const int nw = (int)cdiv64(pieces, 64 * NCH);
   const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1), grid((unsigned)cdiv64(a.M, blk.y));
-  if (!norm) hipLaunchKernelGGL((norm_row<T, 1, NCH, false, false>), grid, blk, 0, st, a);
-  else if (!residual) hipLaunchKernelGGL((norm_row<T, 1, NCH, false, true>), grid, blk, 0, st, a);
-  else if (a.hc == 1) hipLaunchKernelGGL((norm_row<T, 1, NCH, true, true>), grid, blk, 0, st, a);
-  else if (a.hc == 2) hipLaunchKernelGGL((norm_row<T, 2, NCH, true, true>), grid, blk, 0, st, a);
-  else if (a.hc == 4) hipLaunchKernelGGL((norm_row<T, 4, NCH, true, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((norm_row<T, 8, NCH, true, true>), grid, blk, 0, st, a);
+  if (!norm) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, false>), grid, blk, 0, st, a);
+  else if (!residual) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, true>), grid, blk, 0, st, a);
+  else if (a.hc == 1) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, true, true>), grid, blk, 0, st, a);
+  else if (a.hc == 2) hipLaunchKernelGGL((norm_row<T, 2, NCH, AL, true, true>), grid, blk, 0, st, a);
+  else if (a.hc == 4) hipLaunchKernelGGL((norm_row<T, 4, NCH, AL, true, true>), grid, blk, 0, st, a);
+  else hipLaunchKernelGGL((norm_row<T, 8, NCH, AL, true, true>), grid, blk, 0, st, a);
   return (int)hipGetLastError();
 }
 
@@ -1005,10 +1035,9 @@ int forward_of(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
   const bool al = aligned(a, (int)sizeof(typename T::S));
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   if (a.M >= (int64_t)1 << 31) return forward_loop<T, false>(a, residual, norm, st);  // past the largest grid
-  if (!al) return forward_loop<T, false>(a, residual, norm, st);
-  if (pieces <= 1024) return forward_row<T, 1>(a, residual, norm, st);
-  if (pieces <= 2048) return forward_row<T, 2>(a, residual, norm, st);
-  return forward_loop<T, true>(a, residual, norm, st);
+  if (pieces <= 1024) return al ? forward_row<T, 1, true>(a, residual, norm, st) : forward_row<T, 1, false>(a, residual, norm, st);
+  if (pieces <= 2048 && al) return forward_row<T, 2, true>(a, residual, norm, st);
+  return al ? forward_loop<T, true>(a, residual, norm, st) : forward_loop<T, false>(a, residual, norm, st);
 }
 
 int sum_groups(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
@@ -1027,25 +1056,29 @@ int backward_loop(const NormBwdArgs& a, hipStream_t st) {
   return sum_groups(a, groups, st);
 }
 
-template <typename T, int NCH, int THREADS>
+template <typename T, int NCH, int THREADS, bool AL>
 int backward_row(const NormBwdArgs& a, bool residual, hipStream_t st) {
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   const int nw = (int)cdiv64(pieces, 64 * NCH);
   const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1);
   const int64_t groups = bwd_groups(cdiv64(a.M, blk.y));
   const dim3 grid((unsigned)groups);
-  const size_t lds = bwd_lds(residual ? a.hc : 0, NCH, (int)(blk.x * blk.y / 64), vec<T>(), THREADS <= 512, nw == 1);
-  if (!residual) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, false>), grid, blk, lds, st, a);
-  else if (a.hc == 1) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, true>), grid, blk, lds, st, a);
-  else if (a.hc == 2) hipLaunchKernelGGL((norm_bwd_row<T, 2, NCH, THREADS, true>), grid, blk, lds, st, a);
-  else if (a.hc == 4) hipLaunchKernelGGL((norm_bwd_row<T, 4, NCH, THREADS, true>), grid, blk, lds, st, a);
-  else hipLaunchKernelGGL((norm_bwd_row<T, 8, NCH, THREADS, true>), grid, blk, lds, st, a);
+  const size_t lds = bwd_lds(residual ? a.hc : 0, NCH, (int)(blk.x * blk.y / 64), vec<T>(), AL && THREADS <= 512 && NCH == 1, nw == 1);
+  if constexpr (THREADS == 512) {
+    if (residual && a.hc == 8) hipLaunchKernelGGL((norm_bwd_row<T, 8, NCH, THREADS, AL, true>), grid, blk, lds, st, a);
+  }
+  if constexpr (NCH == 1) {
+    if (!residual) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, AL, false>), grid, blk, lds, st, a);
+    else if (a.hc == 1) hipLaunchKernelGGL((norm_bwd_row<T, 1, NCH, THREADS, AL, true>), grid, blk, lds, st, a);
+    else if (a.hc == 2) hipLaunchKernelGGL((norm_bwd_row<T, 2, NCH, THREADS, AL, true>), grid, blk, lds, st, a);
+    else if (a.hc == 4) hipLaunchKernelGGL((norm_bwd_row<T, 4, NCH, THREADS, AL, true>), grid, blk, lds, st, a);
+  }
   return sum_groups(a, groups, st);
 }
 
 template <typename T>
 hipError_t raise_lds() {
-  const void* f[] = {(const void*)norm_bwd_row<T, 4, 1, 512, true>, (const void*)norm_bwd_row<T, 8, 1, 512, true>};
+  const void* f[] = {(const void*)norm_bwd_row<T, 4, 1, 512, true, true>, (const void*)norm_bwd_row<T, 8, 1, 512, true, true>};
   for (const void* k : f) {
     const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, 152 * 1024);
     if (e != hipSuccess) return e;
@@ -1056,12 +1089,14 @@ hipError_t raise_lds() {
 template <typename T>
 int backward_of(const NormBwdArgs& a, bool residual, hipStream_t st) {
   const int64_t pieces = cdiv64(a.hs, vec<T>());
-  if (!aligned(a, (int)sizeof(typename T::S)))
-    return residual ? backward_loop<T, false, true>(a, st) : backward_loop<T, false, false>(a, st);
-  // up to 512 threads a thread has 256 registers, which eight streams need;
-  // above, 128 (some rows then pass through scratch memory)
-  if (pieces <= 512) return backward_row<T, 1, 512>(a, residual, st);
-  if (pieces <= 1024) return backward_row<T, 1, 1024>(a, residual, st);
+  const bool al = aligned(a, (int)sizeof(typename T::S));
+  if (pieces <= 512) return al ? backward_row<T, 1, 512, true>(a, residual, st) : backward_row<T, 1, 512, false>(a, residual, st);
+  if (pieces <= 1024 && residual && a.hc == 8)
+    // eight streams do not fit the 128 registers of 1024 threads: 512 threads
+    // with two pieces each, 179 us instead of 358 at M = 1000, HS = 8192 (bf16)
+    return al ? backward_row<T, 2, 512, true>(a, residual, st) : backward_row<T, 2, 512, false>(a, residual, st);
+  if (pieces <= 1024) return al ? backward_row<T, 1, 1024, true>(a, residual, st) : backward_row<T, 1, 1024, false>(a, residual, st);
+  if (!al) return residual ? backward_loop<T, false, true>(a, st) : backward_loop<T, false, false>(a, st);
   return residual ? backward_loop<T, true, true>(a, st) : backward_loop<T, true, false>(a, st);
 }
 

@@ -118,7 +118,8 @@ def amplification(ref):
 RES_SHAPES = [(hc, hs, m) for hc, hs, m in [
     (1, 1, 3), (2, 3, 5), (8, 8, 2), (4, 67, 33), (1, 128, 1030), (4, 128, 5), (2, 504, 513), (8, 520, 7), (2, 1000, 333),
     (4, 2560, 1), (4, 2560, 16), (4, 2560, 700), (8, 2560, 9), (1, 2560, 64), (2, 4100, 65), (4, 10240, 3),
-    (8, 10240, 2), (1, 24576, 2), (8, 24576, 2)]]
+    (8, 10240, 2), (1, 24576, 2), (8, 24576, 2), (8, 8192, 5), (8, 8187, 3), (4, 8192, 300), (2, 2563, 900),
+    (4, 517, 1700), (8, 16384, 2)]]
 
 
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
