@@ -106,17 +106,18 @@ __device__ __forceinline__ i32x4_t range_words(const void* base, uint32_t bytes)
 // 1 KB from memory to LDS at `lds` (lane l's 16 bytes at lds + 16*l). Written
 // as assembly so that the compiler does not make every LDS read wait for all
 // loads in flight: the kernel waits itself (landed). It writes no register but
-// m0, which nothing else in these kernels uses; m0 needs one wait state before
-// such a load.
+// m0, which nothing else in these kernels uses. m0 needs one wait state before
+// such a load, and a descriptor word that a vector instruction has just written
+// (readfirstlane) five, which the compiler does not add inside assembly.
 __device__ __forceinline__ void load_lds(i32x4_t r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                :
                : "v"(off), "s"(r), "s"(lds)
                : "memory");
 }
 // The same, four bytes a lane (256 bytes).
 __device__ __forceinline__ void load_lds4(i32x4_t r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
                :
                : "v"(off), "s"(r), "s"(lds)
                : "memory");

@@ -1,8 +1,9 @@
 // hcgr_linear.hip -- the 8-bit linear layer (hcgr_linear_forward):
 //   out[m, n] = (sum_k q[m, k]*w[n, k]) * q_scale[m] * w_scale[n] + bias[n]
-// on MFMA. Weight rows are the first (row) operand and
-// tokens the second (column) operand, so a lane ends with four neighbouring
-// output channels of one token.
+// on v_mfma_i32_16x16x64_i8 and v_mfma_i32_32x32x32_i8. Weight rows are the
+// first (row) operand and tokens the second (column) operand, so a lane ends
+// with four neighbouring output channels of one token. Sums are exact; one
+// conversion to float, the scales' product and a fused multiply-add follow.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
