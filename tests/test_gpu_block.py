@@ -558,3 +558,82 @@ def test_other_streams(H):
         b2 = blk.residual_bwd(**i, rrms=f2["rrms"], **d, stream=stream)
         s.synchronize()
         assert all(torch.equal(f[k], f2[k]) for k in f) and all(torch.equal(b[k], b2[k]) for k in b)
+
+
+# ------------------------------------------------- far offsets, many callers --
+def test_offsets_past_32_bits(H):
+    """Tensors of more than 2^32 bytes: the first and last rows, and rows
+    around the 2^31 and 2^32 byte marks."""
+    m, hc, hs = 110000, 8, 2560
+    say("far residual")
+    blk = block(H, hc, hs, BF16)
+    g = gen(20)
+    i = residual_inputs(g, 1, hc, hs, BF16)
+    i["y"], i["inj"] = randn(g, m, hs, dtype=BF16), randn(g, m, hc, dtype=BF16)
+    i["R"] = torch.empty((m, hc * hs), dtype=BF16, device="cuda")
+    for a in range(0, m, 10000):
+        i["R"][a:a + 10000] = randn(g, min(10000, m - a), hc * hs, dtype=BF16)
+    assert i["R"].numel() * 2 > 2 ** 32
+    marks = [0, 1, 52428, 52429, 104857, 104858, m - 1]
+    out = blk.residual(**i)
+    few = {k: (v[marks] if k in ("R", "y", "inj") else v) for k, v in i.items()}
+    ref = B.residual(**few, hc=hc, eps=EPS, rho=RHO)
+    check_residual({k: v[marks] for k, v in out.items()}, ref, True, True)
+    dx = randn(g, m, hs, dtype=BF16)
+    got = blk.residual_bwd(**i, rrms=out["rrms"], dR2=i["R"], dx=dx)
+    want = B.residual_bwd(**few, rrms=out["rrms"][marks], dR2=i["R"][marks], dx=dx[marks], hc=hc, rho=RHO)
+    for k in ("dR", "dy", "dinj"):
+        B.check(got[k][marks], want[k], k)
+
+
+@pytest.mark.parametrize("n,k,m", [(8192, 64, 300000), (16, 32, 1100000), (1048576, 4112, 3), (40000, 48, 60000)])
+def test_linear_offsets_past_32_bits(H, n, k, m):
+    """Outputs or weights of more than 2^32 bytes, and more than 2^20 tokens."""
+    say("far linear", n, k, m)
+    lin = H.Int8Linear(H.LinearConfig(n=n, k=k), 0)
+    i = linear_inputs(gen(21), n, k, m, BF16)
+    out = lin.forward(**i)
+    rows = sorted({0, 1, m // 2, m - 2, m - 1} & set(range(m)) | ({1 << 20, (1 << 20) - 1} if m > 1 << 20 else set()))
+    cols = sorted({0, 1, n // 2, n - 2, n - 1})
+    part = {"q": i["q"][rows], "q_scale": i["q_scale"][rows], "w": i["w"][cols], "w_scale": i["w_scale"][cols],
+            "bias": i["bias"][cols]}
+    B.check(out[rows][:, cols], B.linear(**part), "out", 4)
+
+
+def test_two_threads_on_one_handle(H):
+    """Handles are read-only: two threads call them at once, each on a stream of its own."""
+    import threading
+    m, hc, hs = 900, 2, 1000
+    blk, lin = block(H, hc, hs, BF16), H.Int8Linear(H.LinearConfig(n=300, k=hs), 0)
+    sets, want, got = [], [], [None, None]
+    for t in range(2):
+        g = gen(30 + t)
+        i = residual_inputs(g, m, hc, hs, BF16)
+        d = {"dR2": randn(g, m, hc * hs, dtype=BF16), "dx": randn(g, m, hs, dtype=BF16)}
+        w = lin.quantize(randn(g, 300, hs, dtype=BF16))
+        sets.append((i, d, w))
+
+    def run(t, reps):
+        i, d, w = sets[t]
+        for _ in range(reps):
+            f = blk.residual(**i, quantize=True)
+            b = blk.residual_bwd(**i, rrms=f["rrms"], **d)
+            o = lin.forward(f["q"], f["q_scale"], *w)
+        return {**f, **b, "o": o}
+
+    want = [run(t, 1) for t in range(2)]
+    torch.cuda.synchronize()
+
+    def worker(t):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got[t] = run(t, 20)
+        s.synchronize()
+
+    threads = [threading.Thread(target=worker, args=(t,)) for t in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for t in range(2):
+        assert all(torch.equal(got[t][k], want[t][k]) for k in want[t]), t
