@@ -46,10 +46,10 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v) {
 }
 
 // Four output channels n .. n+3 of token m from their sums. VEC: the row's
-// pieces of four values are aligned and whole; otherwise those below `end`.
-// NT: with the streaming policy, for whole tiles: they outgrow the L2 as they
-// are, and the workgroups of a round write them at the same time (8192x10240x
-// 2560: 245 -> 230 us).
+// pieces of four values are aligned and whole; otherwise those below `end`, at
+// any alignment. NT: with the streaming policy, for outputs that outgrow the
+// L2s: the workgroups of a round write them at the same time (8192x10240x2560:
+// 245 -> 230 us).
 template <int DT, bool VEC, bool NT = false>
 __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int n, float qs, const float (&ws)[4],
                                        const float (&bias)[4], const int (&acc)[4], int end) {
@@ -57,7 +57,7 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int n, fl
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = fmaf((float)acc[i], qs * ws[i], bias[i]);
   const int64_t at = m * a.ld_out + n;
-  if constexpr (VEC) {
+  if (VEC || n + 4 <= end) {
     typedef uint32_t words_t __attribute__((ext_vector_type(DT == 2 ? 4 : 2)));
     words_t w;
     if constexpr (DT == 0) {
@@ -68,9 +68,10 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int n, fl
     } else {
       w = __builtin_bit_cast(words_t, f32x4_t{v[0], v[1], v[2], v[3]});
     }
-    words_t* to = reinterpret_cast<words_t*>(reinterpret_cast<uint8_t*>(a.out) + at * (DT == 2 ? 4 : 2));
-    if constexpr (NT) __builtin_nontemporal_store(w, to);
-    else *to = w;
+    uint8_t* to = reinterpret_cast<uint8_t*>(a.out) + at * (DT == 2 ? 4 : 2);
+    if constexpr (!VEC) __builtin_memcpy(to, &w, sizeof w);  // gfx950 stores at any alignment
+    else if constexpr (NT) __builtin_nontemporal_store(w, reinterpret_cast<words_t*>(to));
+    else *reinterpret_cast<words_t*>(to) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -223,7 +224,7 @@ constexpr int kRing = 4;
 template <int TM, int TN>
 constexpr int tile_lds() { return kRing * stage_bytes<TM, TN>() + kTables; }
 
-template <int DT, int TM, int TN, bool VEC>
+template <int DT, int TM, int TN, bool VEC, bool NT>
 __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile(LinearArgs a, int tiles_m, int tiles_n) {
   extern __shared__ uint8_t lds[];
   constexpr int FM = TM / 64, FN = TN / 64, SB = stage_bytes<TM, TN>(), NB = kRing;
@@ -414,7 +415,7 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
             const i32x4_t c = *reinterpret_cast<const i32x4_t*>(turn + row * (COLS * 4) + ((lane % P) ^ (row % P)) * 16);
             const int ml = wm * (TM / 2) + g * 32 + part * ROWS + row;
             const int v[4] = {c[0], c[1], c[2], c[3]};
-            if (m0 + ml < a.M && n < a.n) store4<DT, VEC, TM * TN >= 256 * 256>(a, m0 + ml, n, table[256 + ml], ws, bias, v, a.n);
+            if (m0 + ml < a.M && n < a.n) store4<DT, VEC, NT>(a, m0 + ml, n, table[256 + ml], ws, bias, v, a.n);
           }
         }
     }
@@ -455,19 +456,21 @@ int run_skinny(const LinearArgs& a, hipStream_t st) {
   return launch_split<DT, MT, 1, kMany>(a, rows, 4, st);
 }
 
-template <int DT, int TM, int TN, bool VEC>
+template <int DT, int TM, int TN, bool VEC, bool NT>
 int launch_tile(const LinearArgs& a, hipStream_t st) {
   const int tm = (int)cdiv64(a.M, TM), tn = (int)cdiv64(a.n, TN);
   // persistent workgroups: as many as the 256 CUs hold at once
   constexpr int kHeld = TM * TN >= 256 * 256 ? 256 : 512;
   const int64_t tiles = cdiv64((int64_t)tm * tn, 8) * 8;
-  hipLaunchKernelGGL((linear_tile<DT, TM, TN, VEC>), dim3((unsigned)std::min<int64_t>(tiles, kHeld)), dim3(256),
+  hipLaunchKernelGGL((linear_tile<DT, TM, TN, VEC, NT>), dim3((unsigned)std::min<int64_t>(tiles, kHeld)), dim3(256),
                      (tile_lds<TM, TN>()), st, a, tm, tn);
   return (int)hipGetLastError();
 }
 template <int DT, int TM, int TN>
 int run_tile(const LinearArgs& a, hipStream_t st) {
-  return pieces_of_four<DT>(a) ? launch_tile<DT, TM, TN, true>(a, st) : launch_tile<DT, TM, TN, false>(a, st);
+  if (!pieces_of_four<DT>(a)) return launch_tile<DT, TM, TN, false, false>(a, st);
+  const bool nt = (double)a.M * a.n * (DT == 2 ? 4 : 2) > 32.0 * 1024 * 1024;  // more than the L2s hold
+  return nt ? launch_tile<DT, TM, TN, true, true>(a, st) : launch_tile<DT, TM, TN, true, false>(a, st);
 }
 
 // The kernel is the one that a model of its time, in microseconds, puts first:
@@ -496,11 +499,13 @@ int run(const LinearArgs& a, hipStream_t st) {
 
 template <int DT>
 int raise_lds() {
-  const void* f[] = {(const void*)linear_tile<DT, 256, 256, true>, (const void*)linear_tile<DT, 256, 256, false>,
-                     (const void*)linear_tile<DT, 128, 128, true>, (const void*)linear_tile<DT, 128, 128, false>,
-                     (const void*)linear_split<DT, 1, 1, 5>,       (const void*)linear_split<DT, 1, 1, 3>,
-                     (const void*)linear_split<DT, 2, 1, 3>,       (const void*)linear_split<DT, 2, 1, 2>,
-                     (const void*)linear_split<DT, 2, 2, 2>,       (const void*)linear_split<DT, 4, 4, 2>};
+  const void* f[] = {
+      (const void*)linear_tile<DT, 256, 256, true, true>,  (const void*)linear_tile<DT, 256, 256, true, false>,
+      (const void*)linear_tile<DT, 256, 256, false, false>, (const void*)linear_tile<DT, 128, 128, true, true>,
+      (const void*)linear_tile<DT, 128, 128, true, false>, (const void*)linear_tile<DT, 128, 128, false, false>,
+      (const void*)linear_split<DT, 1, 1, 5>,              (const void*)linear_split<DT, 1, 1, 3>,
+      (const void*)linear_split<DT, 2, 1, 3>,              (const void*)linear_split<DT, 2, 1, 2>,
+      (const void*)linear_split<DT, 2, 2, 2>,              (const void*)linear_split<DT, 4, 4, 2>};
   for (const void* k : f) {
     const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != hipSuccess) return (int)e;
