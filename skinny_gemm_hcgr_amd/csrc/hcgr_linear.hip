@@ -478,7 +478,7 @@ int run_tile(const LinearArgs& a, hipStream_t st) {
 // own and one for each unit of 128 bytes of K; the kernels for few tokens are
 // also bound by the weights' bytes at 5.2 TB/s. The constants are fitted on
 // one MI355X to N x K = 1024 x 1024 .. 10240 x 2560 and 2560 x 10240, M = 1 ..
-// 2048 (all within a quarter of the measured times). Measured, split 32x32 /
+// 2048 (mostly within a quarter of the measured times). Measured, split 32x32 /
 // split 64x64 / tile 128 / tile 256: 2560x10240 at M = 64: 10.9 / 20 / 47 /
 // 101 us, M = 384: 33 / 21 / 51 / 107, M = 1024: - / 74 / 51 / 113; 10240x2560
 // at M = 384: 37 / 33 / 21 / 39, M = 3000: - / 179 / 116 / 92.
