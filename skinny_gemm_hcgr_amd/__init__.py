@@ -725,17 +725,22 @@ class _Op:
             return self._current(self.device)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def _made(self, stream, *tensors):
-        """Tensors allocated here and used on `stream`: torch must not hand
-        their memory on before that stream is done with them."""
-        if stream is None:
-            return
+    def _on(self, stream, alloc, *args, **kw):
+        """alloc(...) for a call on `stream`: from that stream's memory, so that
+        nothing still running elsewhere holds it, and kept until torch's
+        current stream, which may read the results, is done with it."""
         cuda = self._torch.cuda
+        if stream is None:
+            return alloc(*args, **kw)
         s = cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
-        if s != cuda.current_stream(self.device):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(s)
+        now = cuda.current_stream(self.device)
+        if s == now:
+            return alloc(*args, **kw)
+        with cuda.stream(s):
+            made = alloc(*args, **kw)
+        for t in made.values() if isinstance(made, dict) else made if isinstance(made, tuple) else (made,):
+            t.record_stream(now)
+        return made
 
     def _empty(self, shape, dtype):
         return self._torch.empty(shape, dtype=dtype, device=f"cuda:{self.device}")
@@ -797,9 +802,9 @@ class Block(_Op):
             qs = self._dense("q_scale", out["q_scale"], f32, (M,))
         return x, q, ld_q, qs
 
-    def _ws(self, workspace, M):
+    def _ws(self, workspace, M, stream):
         if workspace is None:
-            return self.workspace(M)
+            return self._on(stream, self.workspace, M)
         if workspace.dtype is not self._torch.uint8 or workspace.get_device() != self.device or \
                 not workspace.is_contiguous():
             self._bad("workspace", workspace, "contiguous uint8")
@@ -810,8 +815,7 @@ class Block(_Op):
         M, hs = x.shape[0], self.cfg.hs
         px, ld_x = self._rows("x", x, self.dtype, M, hs)
         if out is None:
-            out = self.alloc_norm(M, quantize=quantize)
-            self._made(stream, *out.values())
+            out = self._on(stream, self.alloc_norm, M, quantize=quantize)
         xn, q, ld_q, qs = self._norm_outputs(out, M)
         _check(self._lib.hcgr_block_norm(
             self.handle, px, ld_x, self._dense("w", w, self.dtype, (hs,)), M, xn, q, ld_q, qs,
@@ -823,11 +827,8 @@ class Block(_Op):
         M, hs, f32 = x.shape[0], self.cfg.hs, self._f32
         px, ld_x = self._rows("x", x, self.dtype, M, hs)
         if out is None:
-            out = self.alloc_norm_bwd(M)
-            self._made(stream, *out.values())
-        ws = self._ws(workspace, M)
-        if workspace is None:
-            self._made(stream, ws)
+            out = self._on(stream, self.alloc_norm_bwd, M)
+        ws = self._ws(workspace, M, stream)
         _check(self._lib.hcgr_block_norm_bwd(
             self.handle, px, ld_x, self._dense("w", w, self.dtype, (hs,)), self._dense("rrms", rrms, f32, (M,)),
             self._dense("dxn", dxn, self.dtype, (M, hs)), M, self._dense("dx", out.get("dx"), self.dtype, (M, hs)),
@@ -844,8 +845,7 @@ class Block(_Op):
         py, ld_y = self._rows("y", y, dt, M, hs)
         pi, ld_i = self._rows("inj", inj, dt, M, c.hc) if inj is not None else (None, 0)
         if out is None:
-            out = self.alloc_residual(M, norm=w_pre is not None, quantize=quantize)
-            self._made(stream, *out.values())
+            out = self._on(stream, self.alloc_residual, M, norm=w_pre is not None, quantize=quantize)
         x, q, ld_q, qs = self._norm_outputs(out, M)
         _check(self._lib.hcgr_block_residual(
             self.handle, self._dense("R", R, dt, (M, k)), py, ld_y, pi, ld_i,
@@ -864,14 +864,12 @@ class Block(_Op):
         py, ld_y = self._rows("y", y, dt, M, hs)
         pi, ld_i = self._rows("inj", inj, dt, M, c.hc) if inj is not None else (None, 0)
         if out is None:
-            out = self.alloc_residual_bwd(M, gates=inj is not None, post=w_post is not None, pre=w_pre is not None)
-            self._made(stream, *out.values())
+            out = self._on(stream, self.alloc_residual_bwd, M, gates=inj is not None, post=w_post is not None,
+                           pre=w_pre is not None)
         di, ld_di = out.get("dinj"), 0
         if di is not None:
             di, ld_di = self._rows("dinj", di, dt, M, c.hc)
-        ws = self._ws(workspace, M)
-        if workspace is None:
-            self._made(stream, ws)
+        ws = self._ws(workspace, M, stream)
         _check(self._lib.hcgr_block_residual_bwd(
             self.handle, self._dense("R", R, dt, (M, k)), py, ld_y, pi, ld_i,
             self._dense("w_post", w_post, dt, (hs,)), self._dense("w_pre", w_pre, dt, (hs,)),
@@ -903,8 +901,7 @@ class Int8Linear(_Op):
         M, k = x.shape[0], self.cfg.k
         px, ld_x = self._rows("x", x, self.dtype, M, k)
         if out is None:
-            out = self.alloc_quantized(M)
-            self._made(stream, *out)
+            out = self._on(stream, self.alloc_quantized, M)
         q, ld_q = self._rows8("q", out[0], M, k)
         _check(self._lib.hcgr_linear_quantize(
             self.handle, px, ld_x, M, q, ld_q, self._dense("q_scale", out[1], self._f32, (M,)),
@@ -917,8 +914,7 @@ class Int8Linear(_Op):
         pq, ld_q = self._rows8("q", q, M, c.k)
         pw, ld_w = self._rows8("w", w, c.n, c.k)
         if out is None:
-            out = self.alloc_output(M)
-            self._made(stream, out)
+            out = self._on(stream, self.alloc_output, M)
         po, ld_o = self._rows("out", out, self.dtype, M, c.n)
         _check(self._lib.hcgr_linear_forward(
             self.handle, pq, ld_q, self._dense("q_scale", q_scale, f32, (M,)), pw, ld_w,

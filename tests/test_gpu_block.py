@@ -637,3 +637,23 @@ def test_two_threads_on_one_handle(H):
         t.join()
     for t in range(2):
         assert all(torch.equal(got[t][k], want[t][k]) for k in want[t]), t
+
+
+def test_outputs_for_another_stream_are_that_stream_s_memory(H):
+    """A block that torch's current stream has freed but still writes is not
+    handed to a call on another stream."""
+    m, hs = 4096, 2560
+    blk, g = block(H, 1, hs, BF16), gen(41)
+    x, w = randn(g, m, hs, dtype=BF16), randn(g, hs, dtype=BF16, scale=0.1)
+    want = blk.norm(x, w)["x"].clone()
+    big = torch.randn(8192, 8192, device="cuda")
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        torch.cuda.synchronize()
+        held = torch.empty((m, hs), dtype=BF16, device="cuda")
+        torch.mm(big, big)           # keeps the current stream busy
+        held.fill_(7.0)              # pending when the block is freed
+        del held
+        out = blk.norm(x, w, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(out["x"], want)
