@@ -118,10 +118,11 @@ __global__ __launch_bounds__(512) void linear_split(LinearArgs a, int rows, int 
   // Workgroups b, b + 8, b + 16, .. share an XCD: those of one XCD take the
   // tokens of the same channels one after the other, so that the weights come
   // from memory once.
-  const int local = (int)blockIdx.x / 8;
-  const int n0 = (local / tiles_m * 8 + (int)blockIdx.x % 8) * rows;
-  if (n0 >= a.n) return;  // the whole workgroup
-  const int64_t m0 = (int64_t)(local % tiles_m) * (16 * MT);
+  const int tiles = tiles_m * ((a.n + rows - 1) / rows), per = (tiles + 7) / 8;
+  const int tile = (int)blockIdx.x % 8 * per + (int)blockIdx.x / 8;
+  if ((int)blockIdx.x / 8 >= per || tile >= tiles) return;  // the whole workgroup
+  const int n0 = tile / tiles_m * rows;
+  const int64_t m0 = (int64_t)(tile % tiles_m) * (16 * MT);
   const int k16 = (a.k + 15) / 16 * 16, units = (a.k + 127) / 128;
   const int nr = min(rows, a.n - n0), mr = (int)min((int64_t)(16 * MT), a.M - m0);
   // rows past the last are past the range (a pitch is at least k16)
@@ -438,7 +439,7 @@ bool pieces_of_four(const LinearArgs& a) {
 template <int DT, int MT, int NT, int D>
 int launch_split(const LinearArgs& a, int rows, int nw, hipStream_t st) {
   const int tm = (int)cdiv64(a.M, 16 * MT);
-  const dim3 g((unsigned)(cdiv64(cdiv64(a.n, rows), 8) * 8 * tm)), blk((unsigned)nw * 64);
+  const dim3 g((unsigned)(cdiv64(cdiv64(a.n, rows) * tm, 8) * 8)), blk((unsigned)nw * 64);
   hipLaunchKernelGGL((linear_split<DT, MT, NT, D>), g, blk, (size_t)nw * D * (MT + NT) * 2048, st, a, rows, tm,
                      rows % 4 == 0 && pieces_of_four<DT>(a));
   return (int)hipGetLastError();

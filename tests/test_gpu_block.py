@@ -329,7 +329,9 @@ LIN = [  # n, k, m
     (2560, 10240, 1), (10240, 2560, 1), (2560, 10240, 32), (2560, 2560, 5), (320, 10240, 33), (513, 129, 129),
     (1024, 512, 1023), (2500, 640, 513), (4, 131071, 3), (333, 4096, 257), (2560, 320, 2048), (4096, 1040, 1100),
     # few stages of K in many tiles, so that a workgroup's loads run far ahead
-    (8200, 40, 8200), (5000, 100, 3000), (4100, 64, 1300), (2600, 130, 1700), (300, 8, 700), (8192, 200, 600)]
+    (8200, 40, 8200), (5000, 100, 3000), (4100, 64, 1300), (2600, 130, 1700), (300, 8, 700), (8192, 200, 600),
+    # one tile of channels, many of tokens
+    (16, 214, 16336), (40, 72, 5000)]
 
 
 def linear_inputs(g, n, k, m, dt, bias=True, extreme=False):
