@@ -757,6 +757,7 @@ class Block(_Op):
 
     def __init__(self, cfg: BlockConfig = BlockConfig(), device: int = 0):
         super().__init__(cfg, device, hcgr_block_create, hcgr_block_destroy)
+        self._ws_bytes = {}  # workspace bytes by token count
 
     def alloc_norm(self, M: int, *, quantize: bool = False, keep: bool = False) -> dict:
         """``quantize``: q and q_scale in place of x; ``keep``: x as well."""
@@ -791,7 +792,12 @@ class Block(_Op):
 
     def workspace(self, M: int):
         """A workspace for the backward entry points (no initialisation needed)."""
-        return self._empty((hcgr_block_workspace_size(self.handle, M),), self._torch.uint8)
+        n = self._ws_bytes.get(M)
+        if n is None:
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            n = self._ws_bytes[M] = hcgr_block_workspace_size(self.handle, M)
+        return self._empty((n,), self._torch.uint8)
 
     def _norm_outputs(self, out, M):
         hs, f32 = self.cfg.hs, self._f32

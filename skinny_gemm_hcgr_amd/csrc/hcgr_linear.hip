@@ -489,7 +489,7 @@ int run(const LinearArgs& a, hipStream_t st) {
   auto rounds = [&](int tm, int tn) { return (double)cdiv64(cdiv64(a.M, tm) * cdiv64(a.n, tn), 256); };
   const double stream = 3.0 + (double)a.n * a.k / 5.2e6;
   // (more than one tile of tokens: part of the weights comes from memory again)
-  const double t32 = std::max(1.8 + rounds(32, 32) * (0.4 + 0.1 * u), a.M <= 32 ? stream : 1.5 * stream);
+  const double t32 = std::max(1.8 + rounds(32, 32) * (1.2 + 0.08 * u), a.M <= 32 ? stream : 1.5 * stream);
   if (a.M <= 32 && std::max(3.8, stream - 0.1) <= t32) return a.M <= 16 ? run_skinny<DT, 1>(a, st) : run_skinny<DT, 2>(a, st);
   const double t64 = rounds(64, 64) * (4.6 + 0.19 * u), t128 = 1.0 + rounds(128, 128) * (4.4 + 0.55 * u);
   const double t256 = rounds(256, 256) * (14.0 + 1.25 * u), best = std::min({t32, t64, t128, t256});
