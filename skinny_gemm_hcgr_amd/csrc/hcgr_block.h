@@ -20,6 +20,7 @@ struct NormArgs {
   float *q_scale, *rr_post, *rr_pre;  // rr_*: column of each norm, NULL when not wanted
   int rr_ld;                          // floats from one token's r to the next
   int nt = 0;                         // set by the launch: outputs with the streaming policy
+  int64_t m_first = 0;                // likewise: the launch's first row
 };
 
 // Backward of both. For hcgr_block_norm_bwd: residual = false, R = x, w_pre =

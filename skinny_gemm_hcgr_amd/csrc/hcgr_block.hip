@@ -585,7 +585,7 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
   __shared__ float red[2][16];
   __shared__ uint32_t redq[16];
   const int hs = a.hs;
-  const int64_t m = (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y);
+  const int64_t m = a.m_first + (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y);
   if (m >= a.M) return;  // blockDim.y > 1 only without barriers
   const bool wpre = a.w_pre != nullptr, wpost = RES && a.w_post != nullptr;
   const Row<T, AL> rR(a.R, m * a.ld_R, HC, hs), rY(a.y, m * a.ld_y, 1, hs), rG(a.w_post, 0, 1, hs), rW(a.w_pre, 0, 1, hs);
@@ -980,6 +980,8 @@ __global__ __launch_bounds__(THREADS, AL && THREADS <= 512 && NCH == 1 && HC <= 
 
 // ---------------------------------------------------------------- launches --
 constexpr int64_t kMaxGrid = 1 << 20;
+// Threads of a launch in one dimension: HIP takes fewer than 2^32.
+constexpr int64_t kMaxThreads = (int64_t)1 << 31;
 
 bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 bool ld16_ok(int64_t ld, int b) { return ld * b % 16 == 0; }
@@ -1022,21 +1024,26 @@ int forward_row(NormArgs a, bool residual, bool norm, hipStream_t st) {
   a.nt = streamed(a.M, a.hs, residual ? a.hc + 1 : 1, sizeof(typename T::S));
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   const int nw = (int)cdiv64(pieces, 64 * NCH);
-  const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1), grid((unsigned)cdiv64(a.M, blk.y));
-  if (!norm) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, false>), grid, blk, 0, st, a);
-  else if (!residual) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, true>), grid, blk, 0, st, a);
-  else if (a.hc == 1) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, true, true>), grid, blk, 0, st, a);
-  else if (a.hc == 2) hipLaunchKernelGGL((norm_row<T, 2, NCH, AL, true, true>), grid, blk, 0, st, a);
-  else if (a.hc == 4) hipLaunchKernelGGL((norm_row<T, 4, NCH, AL, true, true>), grid, blk, 0, st, a);
-  else hipLaunchKernelGGL((norm_row<T, 8, NCH, AL, true, true>), grid, blk, 0, st, a);
-  return (int)hipGetLastError();
+  const dim3 blk((unsigned)nw * 64, nw == 1 ? 4 : 1);
+  const int64_t rows = kMaxThreads / blk.x * blk.y;  // of a launch; longer calls take several
+  for (; a.m_first < a.M; a.m_first += rows) {
+    const dim3 grid((unsigned)cdiv64(std::min(rows, a.M - a.m_first), blk.y));
+    if (!norm) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, false>), grid, blk, 0, st, a);
+    else if (!residual) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, false, true>), grid, blk, 0, st, a);
+    else if (a.hc == 1) hipLaunchKernelGGL((norm_row<T, 1, NCH, AL, true, true>), grid, blk, 0, st, a);
+    else if (a.hc == 2) hipLaunchKernelGGL((norm_row<T, 2, NCH, AL, true, true>), grid, blk, 0, st, a);
+    else if (a.hc == 4) hipLaunchKernelGGL((norm_row<T, 4, NCH, AL, true, true>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((norm_row<T, 8, NCH, AL, true, true>), grid, blk, 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+  }
+  return (int)hipSuccess;
 }
 
 template <typename T>
 int forward_of(const NormArgs& a, bool residual, bool norm, hipStream_t st) {
   const bool al = aligned(a, (int)sizeof(typename T::S));
   const int64_t pieces = cdiv64(a.hs, vec<T>());
-  if (a.M >= (int64_t)1 << 31) return forward_loop<T, false>(a, residual, norm, st);  // past the largest grid
   if (pieces <= 1024) return al ? forward_row<T, 1, true>(a, residual, norm, st) : forward_row<T, 1, false>(a, residual, norm, st);
   if (pieces <= 2048 && al) return forward_row<T, 2, true>(a, residual, norm, st);
   return al ? forward_loop<T, true>(a, residual, norm, st) : forward_loop<T, false>(a, residual, norm, st);

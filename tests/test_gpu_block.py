@@ -659,3 +659,21 @@ def test_outputs_for_another_stream_are_that_stream_s_memory(H):
         out = blk.norm(x, w, stream=s)
         torch.cuda.synchronize()
         assert torch.equal(out["x"], want)
+
+
+def test_more_rows_than_one_launch_takes(H):
+    """Past 2^28 rows of one value, four to a workgroup of 64 x 4 threads, a
+    launch would pass 2^32 threads: the call takes several. Every row is
+    written, and the rows around each launch's ends are right."""
+    m = (1 << 28) + 37
+    say("many rows", m)
+    blk, g = block(H, 1, 1, BF16), gen(22)
+    x, w = randn(g, m, 1, dtype=BF16, scale=3.0), randn(g, 1, dtype=BF16, scale=0.2)
+    out = {"x": torch.full((m, 1), float("nan"), dtype=BF16, device="cuda"),
+           "rrms": torch.full((m,), float("nan"), device="cuda")}
+    blk.norm(x, w, out=out)
+    assert bool(out["x"].isfinite().all()) and bool(out["rrms"].isfinite().all())
+    rows = torch.tensor([r + d for r in (0, 1 << 27, 1 << 28, m) for d in range(-6, 6) if 0 <= r + d < m], device="cuda")
+    ref = B.norm(x[rows], w, EPS)
+    B.check(out["x"][rows], ref["x"], "x")
+    B.check(out["rrms"][rows], ref["rrms"], "rrms")
