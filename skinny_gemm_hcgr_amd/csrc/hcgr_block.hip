@@ -138,9 +138,14 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v, uint32_t* red) {
 __device__ __forceinline__ float rrms_of(float sum, int hs, float eps) {
   return 1.0f / sqrtf(sum / (float)hs + eps);
 }
-// 2*sigmoid(inj/HC), and its derivative in inj
+// 2*sigmoid(inj/HC), and its derivative in inj: an even function, from e =
+// exp(-|inj|/HC) as 2*e/(1 + e)^2/HC. (iw*(1 - iw/2)/HC, from a gate iw that is
+// rounded near 2, loses all its digits towards inj/HC = 17.)
 __device__ __forceinline__ float gate(float inj, int hc) { return 2.0f / (1.0f + expf(-inj / (float)hc)); }
-__device__ __forceinline__ float gate_slope(float iw, int hc) { return iw * (1.0f - 0.5f * iw) / (float)hc; }
+__device__ __forceinline__ float gate_slope(float inj, int hc) {
+  const float e = expf(-fabsf(inj) / (float)hc), r = 1.0f / (1.0f + e);
+  return 2.0f / (float)hc * e * r * r;
+}
 
 // ---------------------------------------------------------- quantization --
 // Magnitudes are compared as their bit patterns (an infinity or a NaN is
@@ -421,8 +426,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_rows(NormBwdArgs a) {
         for (int s = 0; s < row.hc; ++s) {
           const float diw = sums[s] + (row.dx ? duz : 0.0f);
           m_post += row.iw[s] * diw;
-          if (a.dinj)
-            reinterpret_cast<typename T::S*>(a.dinj)[m * a.ld_dinj + s] = down<T>(diw * gate_slope(row.iw[s], row.hc));
+          if (a.dinj) {
+            const float inj = up(reinterpret_cast<const typename T::S*>(a.inj)[m * a.ld_inj + s]);
+            reinterpret_cast<typename T::S*>(a.dinj)[m * a.ld_dinj + s] = down<T>(diw * gate_slope(inj, row.hc));
+          }
         }
       }
       rows[2 * m] = m_pre;
@@ -719,7 +726,11 @@ __global__ __launch_bounds__(THREADS, AL && THREADS <= 512 && NCH == 1 && HC <= 
   constexpr bool AHEAD = AL && THREADS <= 512 && NCH == 1;
   constexpr int L = bwd_loads(RES ? HC : 0) * NCH;  // a wave's loads a row, 1 KB each
   __shared__ float red[2][16 * N];
-  extern __shared__ uint8_t ring[];  // [waves][L KB]; at the end the sums of one-wave rows
+  // The slopes of a row's gates, each for the thread that forms it and writes its
+  // dinj: the row's threads 0 .. HC - 1, in wave 0 or, of one-wave rows, in wave y.
+  // (Kept in registers until then they spill: 4 streams in bf16 3 -> 11 registers.)
+  __shared__ float slopes[4][HC];
+  extern __shared__ __attribute__((aligned(16))) uint8_t ring[];  // [waves][L KB]; at the end the sums of one-wave rows
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.y * blockDim.x + threadIdx.x) / 64), lane = (int)threadIdx.x % 64;
   const uint8_t* mine = ring + wave * (L * 1024) + lane * 16;
   const uint32_t mine0 = (uint32_t)(uintptr_t)(lds_u8_t*)ring + (uint32_t)(wave * (L * 1024));
@@ -792,7 +803,23 @@ __global__ __launch_bounds__(THREADS, AL && THREADS <= 512 && NCH == 1 && HC <= 
   if constexpr (AHEAD) fetch(m0);
   for (int64_t m = m0; m < a.M; m += stride) {
     const Scalars now = sc;
+    const float ry = now.ry, ru = now.ru;
+    float iw[HC], iwm = 0.0f;
+    auto gates = [&]() {
+#pragma unroll
+      for (int s = 0; s < HC; ++s) {
+        iw[s] = RES && a.inj ? gate(up(now.inj[s]), HC) : 1.0f;
+        iwm += iw[s] * (1.0f / (float)HC);
+      }
+      if (RES && a.dinj && threadIdx.x < HC) {
+        float inj = up(now.inj[0]);
+#pragma unroll
+        for (int s = 1; s < HC; ++s) inj = (int)threadIdx.x == s ? up(now.inj[s]) : inj;
+        slopes[wave][threadIdx.x] = gate_slope(inj, HC);
+      }
+    };
     if constexpr (AHEAD) {
+      gates();  // before the next row's loads, which the wait for the logits would take in
       // the loads are older than the row before's HC + 1 stores a piece, which
       // may still be on their way (the norm's one store is optional)
       if (RES && m != m0) landed<(HC + 1) * NCH>();
@@ -813,15 +840,9 @@ __global__ __launch_bounds__(THREADS, AL && THREADS <= 512 && NCH == 1 && HC <= 
       fetch(m + stride);
     } else {
       fetch(m);
+      gates();
     }
     sc = scalars(m + stride);
-    const float ry = now.ry, ru = now.ru;
-    float iw[HC], iwm = 0.0f;
-#pragma unroll
-    for (int s = 0; s < HC; ++s) {
-      iw[s] = RES && a.inj ? gate(up(now.inj[s]), HC) : 1.0f;
-      iwm += iw[s] * (1.0f / (float)HC);
-    }
     // u, and the row sums B_s, A, C, D
     float u[NCH][V], sums[N] = {};
 #pragma unroll
@@ -877,8 +898,8 @@ __global__ __launch_bounds__(THREADS, AL && THREADS <= 512 && NCH == 1 && HC <= 
       for (int s = 0; s < HC; ++s) {
         const float diw = sums[s] + duz;
         m_post += iw[s] * diw;
-        if (a.dinj && threadIdx.x == 0)
-          reinterpret_cast<S*>(a.dinj)[m * a.ld_dinj + s] = down<T>(diw * gate_slope(iw[s], HC));
+        if (a.dinj && (int)threadIdx.x == s)
+          reinterpret_cast<S*>(a.dinj)[m * a.ld_dinj + s] = down<T>(diw * slopes[wave][s]);
       }
       m_post /= (float)hs;
     }

@@ -175,6 +175,27 @@ def test_residual_parts(H, hc, hs, m, gates, post, pre, from_R2):
         B.check(got[k], want[k], k, B.C_ROW + (m if k.startswith("dw") else 0))
 
 
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("hc,hs", [(1, 1), (2, 8), (4, 100), (4, 2560), (8, 2560), (2, 40000)])
+def test_gradient_of_gates_far_from_zero(H, hc, hs, dt):
+    """inj/HC up to +-20, z and dR2 positive, so that the sum's terms do not
+    cancel and the bound is relative to the gradient itself. For large positive
+    logits the slope of the gate is far below the gate's own rounding."""
+    say("gates", hc, hs, dt)
+    steps = torch.tensor([-20.0, -16, -12, -8, -3, 0, 3, 8, 12, 16, 20], device="cuda")
+    m, g = len(steps), gen(hc + hs)
+    inj = (torch.stack([steps.roll(s) for s in range(hc)], 1) * hc).to(dt)  # all of them exact in 8 bits
+    assert torch.equal(inj.float(), torch.stack([steps.roll(s) for s in range(hc)], 1) * hc)
+    scale = 1.0 if dt is not FP16 else 2.0 ** 14 / hs  # sums that keep slope * sum a normal number of 16 bits
+    y, dR2 = (0.5 + torch.rand(m, k, generator=g, device="cuda") for k in (hs, hc * hs))
+    i = {"R": randn(g, m, hc * hs, dtype=dt), "y": y.to(dt), "inj": inj, "w_post": None, "w_pre": None}
+    d = {"dR2": (dR2 * scale).to(dt), "dx": None}
+    ref = B.residual_bwd(**i, rrms=None, **d, hc=hc, rho=RHO)
+    got = block(H, hc, hs, dt).residual_bwd(**i, rrms=None, **d)
+    B.check(got["dinj"], ref["dinj"], "dinj")
+    B.check(got["dy"], ref["dy"], "dy")
+
+
 def test_plain_combine_is_the_op_s_combine(H):
     """Without norms and with a residual scale of 1 the operator is COMBINE."""
     m, hc, hs = 50, 4, 2560
