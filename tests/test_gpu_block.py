@@ -432,6 +432,42 @@ def test_quantize_ties_go_to_even(H):
     assert float(s) == 1.0 and q.tolist() == [[127, 0, 2, 2, 0, -2, -126, 126]]
 
 
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("k", [256, 2000, 20480])
+def test_quantize_ties_at_any_scale(H, k, dt):
+    """Every scale s whose s*127 and (i + 1/2)*s the type holds: the quotients
+    are exact ties, whatever 1/s is."""
+    say("ties", k, dt)
+    bits = {BF16: 8, FP16: 11, FP32: 24}[dt]
+    steps = [s for s in range(1, 1 << min(bits - 7, 12)) if s * 127 < 1 << bits] + [0.25, 0.5]
+    half = torch.arange(-126.5, 127.5, 1.0)
+    x = torch.zeros(len(steps), k)
+    x[:, 0] = 127 * torch.tensor(steps)
+    x[:, 1:255] = half[None, :] * torch.tensor(steps)[:, None]
+    held = x.to(dt).float() == x  # the others (many bits) are left out
+    x = torch.where(held, x, 0.0)
+    assert bool(held[:, 0].all()) and int((x[:, 1:] != 0).sum()) >= 60 * len(steps)
+    lin = H.Int8Linear(H.LinearConfig(n=8, k=k, dtype=code(H, dt)), 0)
+    q, s = lin.quantize(x.to(dt).cuda())
+    assert torch.equal(s.cpu(), torch.tensor(steps, dtype=FP32))
+    want = torch.round(x.double() / torch.tensor(steps, dtype=torch.float64)[:, None])  # half to even
+    assert torch.equal(q.cpu().double(), want)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("k,m", [(2560, 300), (67, 3000), (20480, 40)])
+def test_quantize_is_the_rounded_quotient(H, k, m, dt):
+    """q is v/q_scale in 32 bits, rounded: the remainder step leaves the quotient
+    within 2^-44 of itself, so that only a quotient that close to the middle of
+    two 32-bit values next to a half could differ (one in some 10^8)."""
+    lin = H.Int8Linear(H.LinearConfig(n=8, k=k, dtype=code(H, dt)), 0)
+    x = randn(gen(k + m), m, k, dtype=dt, scale=3.0)
+    q, s = lin.quantize(x)
+    x, s = x.float().cpu(), s.cpu()
+    assert torch.equal(s, x.abs().amax(1) / 127)
+    assert torch.equal(q.cpu().float(), torch.round(x / s[:, None]))
+
+
 # ------------------------------------------------------- refusals in Python --
 def test_wrong_tensors_are_refused(H):
     blk = block(H, 2, 64, BF16)
