@@ -531,6 +531,9 @@ hcgr_status hcgr_linear_quantize(hcgr_linear_handle h, const void* x, int64_t ld
  *   ignored.
  *   q_scale [M], w_scale [N] float; bias [N] dtype or NULL;
  *   out [M, ld_out] dtype, columns 0..N-1 written, ld_out >= N.
+ * In 32 bits, in the order (sum * w_scale) * q_scale + bias, the last product
+ * and the addition rounded once: exact sums and any q_scale stay in range with
+ * a w_scale that is 0 or from 2^-126 to 2^96.
  * Needs no workspace. Errors as hcgr_block_norm. */
 hcgr_status hcgr_linear_forward(hcgr_linear_handle h, const int8_t* q, int64_t ld_q, const float* q_scale,
                                 const int8_t* w, int64_t ld_w, const float* w_scale, const void* bias,

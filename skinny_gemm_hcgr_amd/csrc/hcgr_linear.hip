@@ -3,7 +3,11 @@
 // on v_mfma_i32_16x16x64_i8 and v_mfma_i32_32x32x32_i8. Weight rows are the
 // first (row) operand and tokens the second (column) operand, so a lane ends
 // with four neighbouring output channels of one token. Sums are exact; one
-// conversion to float, the scales' product and a fused multiply-add follow.
+// conversion to float, the product with w_scale and a fused multiply-add with
+// q_scale and bias follow. (The scales' product, formed first, would leave the
+// range of 32 bits where the result does not: below 2^-126 it loses bits, above
+// 2^128 a zero sum gives NaN. A sum is 0 or at least 1, so its product with any
+// normal w_scale below 2^97 stays inside.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -55,7 +59,7 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int64_t m, int n, fl
                                        const float (&bias)[4], const int (&acc)[4], int end) {
   float v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = fmaf((float)acc[i], qs * ws[i], bias[i]);
+  for (int i = 0; i < 4; ++i) v[i] = fmaf((float)acc[i] * ws[i], qs, bias[i]);
   const int64_t at = m * a.ld_out + n;
   if (VEC || n + 4 <= end) {
     typedef uint32_t words_t __attribute__((ext_vector_type(DT == 2 ? 4 : 2)));

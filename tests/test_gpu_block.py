@@ -396,6 +396,25 @@ def test_linear_largest_sums(H):
         assert bool((out == float(k) * 2 ** 14).all())  # 131071 * 2^14 is a 32-bit float
 
 
+@pytest.mark.parametrize("n,k,m", [(100, 300, 5), (64, 300, 1000), (2560, 1000, 600)])
+@pytest.mark.parametrize("eq,ew", [(-90, -50), (-50, -90), (-140, 60), (100, -120), (60, -30), (90, 50), (30, 95)])
+def test_linear_scales_far_from_one(H, n, k, m, eq, ew):
+    """Scales whose product leaves the range of 32 bits (or whose q_scale is
+    subnormal) where the results do not; where results would, the tokens are
+    zero: bias alone."""
+    say("scales", n, k, m, eq, ew)
+    lin = H.Int8Linear(H.LinearConfig(n=n, k=k, dtype=H.HCGR_FP32), 0)
+    i = linear_inputs(gen(n + m), n, k, m, FP32)
+    if eq + ew > 60:
+        i["q"].zero_()
+    g = gen(eq + 200)
+    i["q_scale"] = (1 + torch.rand(m, generator=g, device="cuda")) * 2.0 ** eq
+    i["w_scale"] = (1 + torch.rand(n, generator=g, device="cuda")) * 2.0 ** ew
+    i["bias"] *= 2.0 ** max(-120, min(60, eq + ew + 10))
+    # the sum's conversion, its product with w_scale, and one rounding of the rest
+    B.check(lin.forward(**i), B.linear(**i), "out", 2)
+
+
 @pytest.mark.parametrize("m", [1, 20, 200, 700])
 def test_linear_strided(H, m):
     n, k, dt = 200, 300, BF16
