@@ -799,8 +799,10 @@ class Block(_Op):
             n = self._ws_bytes[M] = hcgr_block_workspace_size(self.handle, M)
         return self._empty((n,), self._torch.uint8)
 
-    def _norm_outputs(self, out, M):
+    def _norm_outputs(self, out, M, quantize):
         hs, f32 = self.cfg.hs, self._f32
+        if quantize and out.get("q") is None:
+            raise ValueError("quantize: out has no q (alloc_norm or alloc_residual with quantize=True makes it)")
         x = self._dense("x", out.get("x"), self.dtype, (M, hs))
         q, ld_q, qs = out.get("q"), 0, None
         if q is not None:
@@ -817,12 +819,13 @@ class Block(_Op):
         return workspace
 
     def norm(self, x, w, *, quantize: bool = False, out: dict | None = None, stream=None) -> dict:
-        """x [M, HS] (rows may be strided) -> x or (q, q_scale), and rrms."""
+        """x [M, HS] (rows may be strided) -> x or (q, q_scale), and rrms. With
+        ``out`` what it holds of x and q is written; ``quantize`` then asks for q."""
         M, hs = x.shape[0], self.cfg.hs
         px, ld_x = self._rows("x", x, self.dtype, M, hs)
         if out is None:
             out = self._on(stream, self.alloc_norm, M, quantize=quantize)
-        xn, q, ld_q, qs = self._norm_outputs(out, M)
+        xn, q, ld_q, qs = self._norm_outputs(out, M, quantize)
         _check(self._lib.hcgr_block_norm(
             self.handle, px, ld_x, self._dense("w", w, self.dtype, (hs,)), M, xn, q, ld_q, qs,
             self._dense("rrms", out.get("rrms"), self._f32, (M,)), self._raw(stream)), "hcgr_block_norm")
@@ -845,14 +848,17 @@ class Block(_Op):
     def residual(self, R, y, inj=None, w_post=None, w_pre=None, *, quantize: bool = False, out: dict | None = None,
                  stream=None) -> dict:
         """R [M, HC*HS], y [M, HS], inj [M, HC] (rows of y and inj may be strided)
-        -> R2, rrms, and with w_pre the next norm as x or (q, q_scale)."""
+        -> R2, rrms, and with w_pre the next norm as x or (q, q_scale); ``out``
+        and ``quantize`` as in ``norm``."""
         c, dt = self.cfg, self.dtype
+        if quantize and w_pre is None:
+            raise ValueError("quantize: there is no next norm (w_pre is None)")
         M, hs, k = R.shape[0], c.hs, c.hc * c.hs
         py, ld_y = self._rows("y", y, dt, M, hs)
         pi, ld_i = self._rows("inj", inj, dt, M, c.hc) if inj is not None else (None, 0)
         if out is None:
             out = self._on(stream, self.alloc_residual, M, norm=w_pre is not None, quantize=quantize)
-        x, q, ld_q, qs = self._norm_outputs(out, M)
+        x, q, ld_q, qs = self._norm_outputs(out, M, quantize)
         _check(self._lib.hcgr_block_residual(
             self.handle, self._dense("R", R, dt, (M, k)), py, ld_y, pi, ld_i,
             self._dense("w_post", w_post, dt, (hs,)), self._dense("w_pre", w_pre, dt, (hs,)), M,

@@ -512,6 +512,24 @@ def test_wrong_tensors_are_refused(H):
     assert e.value.status == H.HCGR_ERR_INVALID_ARGUMENT
 
 
+def test_quantize_that_cannot_be_answered_is_refused(H):
+    blk, g = block(H, 2, 64, BF16), gen(50)
+    i = residual_inputs(g, 4, 2, 64, BF16)
+    x, w = i["y"], i["w_pre"]
+    plain, both = blk.alloc_norm(4), blk.alloc_norm(4, quantize=True, keep=True)
+    with pytest.raises(ValueError, match="quantize"):
+        blk.norm(x, w, quantize=True, out=plain)
+    with pytest.raises(ValueError, match="quantize"):
+        blk.residual(**i, quantize=True, out=blk.alloc_residual(4))
+    with pytest.raises(ValueError, match="quantize"):
+        blk.residual(i["R"], x, i["inj"], i["w_post"], None, quantize=True)
+    with pytest.raises(ValueError, match="quantize"):
+        blk.residual(i["R"], x, i["inj"], i["w_post"], None, quantize=True, out=blk.alloc_residual(4, norm=False))
+    want = blk.norm(x, w, quantize=True)
+    for out in (blk.norm(x, w, quantize=True, out=both), blk.norm(x, w, out=both)):
+        assert torch.equal(out["q"], want["q"]) and torch.equal(out["x"], blk.norm(x, w)["x"])
+
+
 # --------------------------------------------------------------- as a layer --
 class Layer:
     """mix -> norm (quantized) -> linear -> SiLU -> quantize -> linear ->
