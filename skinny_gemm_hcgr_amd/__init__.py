@@ -769,8 +769,13 @@ class Block(_Op):
             out["x"] = self._empty((M, hs), self.dtype)
         return out
 
+    def _weight_grad(self, M):
+        """float32 [HS]. A call on no tokens writes nothing: their sum is zero."""
+        dw = self._empty((self.cfg.hs,), self._f32)
+        return dw if M else dw.zero_()
+
     def alloc_norm_bwd(self, M: int) -> dict:
-        return {"dx": self._empty((M, self.cfg.hs), self.dtype), "dw": self._empty((self.cfg.hs,), self._f32)}
+        return {"dx": self._empty((M, self.cfg.hs), self.dtype), "dw": self._weight_grad(M)}
 
     def alloc_residual(self, M: int, *, norm: bool = True, quantize: bool = False, keep: bool = False) -> dict:
         """``norm``: the next norm is wanted (w_pre is given)."""
@@ -780,14 +785,14 @@ class Block(_Op):
         return out
 
     def alloc_residual_bwd(self, M: int, *, gates: bool = True, post: bool = True, pre: bool = True) -> dict:
-        c, f32 = self.cfg, self._f32
+        c = self.cfg
         out = {"dR": self._empty((M, c.k), self.dtype), "dy": self._empty((M, c.hs), self.dtype)}
         if gates:
             out["dinj"] = self._empty((M, c.hc), self.dtype)
         if post:
-            out["dw_post"] = self._empty((c.hs,), f32)
+            out["dw_post"] = self._weight_grad(M)
         if pre:
-            out["dw_pre"] = self._empty((c.hs,), f32)
+            out["dw_pre"] = self._weight_grad(M)
         return out
 
     def workspace(self, M: int):
@@ -832,7 +837,8 @@ class Block(_Op):
         return out
 
     def norm_bwd(self, x, w, rrms, dxn, *, out: dict | None = None, workspace=None, stream=None) -> dict:
-        """Gradients dx [M, HS] and dw [HS] (float32, summed over the tokens) of ``norm``."""
+        """Gradients dx [M, HS] and dw [HS] (float32, summed over the tokens) of
+        ``norm``. With no tokens, dw of a given ``out`` stays as it is."""
         M, hs, f32 = x.shape[0], self.cfg.hs, self._f32
         px, ld_x = self._rows("x", x, self.dtype, M, hs)
         if out is None:

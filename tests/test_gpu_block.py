@@ -271,6 +271,23 @@ def test_empty_batch(H):
     assert lin.forward(q, torch.empty(0, device="cuda"), wq, torch.ones(32, device="cuda")).shape == (0, 32)
 
 
+def test_weight_gradients_of_an_empty_batch_are_zero(H):
+    hs = 256
+    blk = block(H, 4, hs, BF16)
+    w = torch.zeros(hs, dtype=BF16, device="cuda")
+    e = {n: torch.empty((0, n), dtype=BF16, device="cuda") for n in (hs, 4 * hs, 4)}
+    rr = torch.empty((0, 2), device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        held = torch.full((64, hs), 7.0, device="cuda")  # what a new tensor of this size may hold
+        del held
+        got = [blk.norm_bwd(e[hs], w, rr[:, 0], e[hs], stream=stream)["dw"]]
+        out = blk.residual_bwd(e[4 * hs], e[hs], e[4], w, w, rr, e[4 * hs], e[hs], stream=stream)
+        got += [out["dw_post"], out["dw_pre"]]
+        torch.cuda.synchronize()
+        for t in got:
+            assert t.shape == (hs,) and not bool(t.any())
+
+
 def test_zero_rows_and_values_that_are_not_finite(H):
     """A zero row: r = 1/sqrt(eps), q = 0 with scale 0. A row with an infinity
     or a NaN spoils itself and no other row, and its quantized form says so."""
