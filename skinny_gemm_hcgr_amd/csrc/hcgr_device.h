@@ -93,6 +93,14 @@ __device__ __forceinline__ void st_f32(float* p, float v, int wt) {
 // outstanding global->LDS loads, which may stay in flight across it (their
 // target is read only after an explicit full wait).
 __device__ __forceinline__ void lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// Between an LDS access of some lanes of a wave and one of other lanes to the
+// same place. A wave's LDS accesses run in order, so the hardware needs nothing;
+// it keeps the compiler from moving them past each other.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 // logistic function through the hardware 2^x and reciprocal: 1/(1 + 2^(-v*log2 e))
 __device__ __forceinline__ float sigmoid_f(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 

@@ -414,6 +414,7 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
                     i32x4_t{c[q * 4], c[q * 4 + 1], c[q * 4 + 2], c[q * 4 + 3]};
               }
           }
+          wave_sync();  // lanes read what others wrote
 #pragma unroll
           for (int k = 0; k < ROWS * P / 64; ++k) {
             const int row = k * (64 / P) + lane / P;
@@ -422,6 +423,7 @@ __global__ __launch_bounds__(256, TM * TN >= 256 * 256 ? 1 : 2) void linear_tile
             const int v[4] = {c[0], c[1], c[2], c[3]};
             if (m0 + ml < a.M && n < a.n) store4<DT, VEC, NT>(a, m0 + ml, n, table[256 + ml], ws, bias, v, a.n);
           }
+          wave_sync();  // and the next part writes where they read
         }
     }
     lds_sync();  // every wave is done with the slot
