@@ -96,17 +96,14 @@ hcgr_status check_device(int device) {
 }
 
 hcgr_status enter_device(int device, void* stream, int* prev) {
-  int dev = -1;
   hipError_t e;
   if (stream) {
+    int dev = -1;
     e = hipStreamGetDevice(reinterpret_cast<hipStream_t>(stream), &dev);
     if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipStreamGetDevice: %s", hipGetErrorString(e));
-  } else {
-    e = hipGetDevice(&dev);
-    if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
+    if (dev != device)
+      return fail(HCGR_ERR_INVALID_ARGUMENT, "stream belongs to device %d, handle to device %d", dev, device);
   }
-  if (dev != device)
-    return fail(HCGR_ERR_INVALID_ARGUMENT, "stream belongs to device %d, handle to device %d", dev, device);
   int cur = -1;
   e = hipGetDevice(&cur);
   if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));

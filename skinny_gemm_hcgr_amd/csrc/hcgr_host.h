@@ -35,8 +35,8 @@ hcgr_status check_ptrs(const PtrCheck* ptrs, int n);
 // HCGR_OK when `device` exists and is a gfx950.
 hcgr_status check_device(int device);
 
-// Checks that `stream` (NULL: the current device's default stream) belongs to
-// `device` and makes that device current; *prev is the caller's device.
+// Checks that `stream` (NULL: the default stream of `device`) belongs to `device`
+// and makes that device current; *prev is the caller's device.
 hcgr_status enter_device(int device, void* stream, int* prev);
 void restore_device(int device, int prev);
 

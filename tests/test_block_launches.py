@@ -111,3 +111,24 @@ def test_other_launches_of_the_longest_calls(rec, hs, hc, dtype):
         check_sizes(backward(rec, M, hs, hc, dtype))
         check_sizes(linear(rec, M, hs, 2560, dtype))
         check_sizes(linear(rec, M, hs, 16, dtype))
+
+
+CALLS = {"norm": lambda rec, **q: norm(rec, 100, 2560, **q), "residual": lambda rec, **q: residual(rec, 100, 512, 4, **q),
+         "quantize": lambda rec, **q: quantize(rec, 100, 777, **q), "backward": lambda rec, **q: backward(rec, 100, 512, 4, **q),
+         "linear": lambda rec, **q: linear(rec, 100, 2560, 512, **q)}
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_the_handle_s_device(rec, call, current):
+    """Whatever device is current: on a stream of the handle's device, or on
+    that device's default stream (NULL); the caller's device stays current."""
+    for device in (0, 1):
+        for stream in (0, device * 16 + 3):
+            a = CALLS[call](rec, device=device, current=current, stream=stream)
+            assert a["status"] == H.HCGR_OK, (device, stream, a["error"])
+            assert a["launches"] and a["current"] == current
+            assert all(la["device"] == device and la["stream"] == stream for la in a["launches"])
+        a = CALLS[call](rec, device=device, current=current, stream=(1 - device) * 16 + 3)
+        assert a["status"] == H.HCGR_ERR_INVALID_ARGUMENT and "stream belongs to" in a["error"]
+        assert not a["launches"] and a["current"] == current
