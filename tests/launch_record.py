@@ -28,10 +28,14 @@ class Recorder:
         self.p = subprocess.Popen([sys.executable, os.path.abspath(__file__), build(folder)], stdin=subprocess.PIPE,
                                   stdout=subprocess.PIPE, text=True)
 
-    def ask(self, **request) -> dict:
+    def ask(self, **request):
         self.p.stdin.write(json.dumps(request) + "\n")
         self.p.stdin.flush()
         return json.loads(self.p.stdout.readline())
+
+    def kernels(self) -> list:
+        """Every kernel the library holds."""
+        return self.ask()
 
     def close(self):
         self.p.stdin.close()
@@ -63,12 +67,14 @@ def _answer(rt, H, q):
 
 def main():
     rt = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)  # before the library, which then binds to it
-    rt.recorded_launches.restype = ctypes.c_char_p
+    rt.recorded_launches.restype = rt.registered_kernels.restype = ctypes.c_char_p
     sys.path.insert(0, ROOT)
     import skinny_gemm_hcgr_amd as H
     H.load_library()
     for line in sys.stdin:
-        print(json.dumps(_answer(rt, H, json.loads(line))), flush=True)
+        q = json.loads(line)
+        got = _answer(rt, H, q) if q else rt.registered_kernels().decode().splitlines()
+        print(json.dumps(got), flush=True)
 
 
 if __name__ == "__main__":

@@ -32,6 +32,12 @@ extern "C" {
 
 const char* recorded_launches() { return notes.c_str(); }
 void forget_launches() { notes.clear(); }
+const char* registered_kernels() {
+  static std::string all;
+  all.clear();
+  for (const auto& k : kernels) all += k.second + "\n";
+  return all.c_str();
+}
 
 void** __hipRegisterFatBinary(const void*) {
   static void* handle;

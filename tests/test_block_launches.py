@@ -1,6 +1,7 @@
 """The launches of the block operators on the CPU: what each call sends to the
 device, recorded by a stand-in for the HIP runtime."""
 import os
+import re
 
 import pytest
 
@@ -58,6 +59,14 @@ def backward(rec, M, hs, hc, dtype=H.HCGR_BF16, **q):
                                                                   M * k, M * row, M * hc * b, hs * 4, hs * 4, n)
     return rec.ask(config="BlockConfig", values={"hc": hc, "hs": hs, "dtype": dtype}, call="hcgr_block_residual_bwd",
                    args=[R, y, hs, inj, hc, w, w, rr, dR2, dx, M, dR, dy, dinj, hc, dw, dw2, ws, n], **q)
+
+
+def norm_backward(rec, M, hs, dtype=H.HCGR_BF16, **q):
+    b = BYTES[dtype]
+    ws_bytes = H.hcgr_block_workspace_size_for(H.BlockConfig(hc=1, hs=hs, dtype=dtype), M)
+    x, w, rr, d, dx, dw, ws = places(M * hs * b, hs * b, 4 * M, M * hs * b, M * hs * b, 4 * hs, ws_bytes)
+    return rec.ask(config="BlockConfig", values={"hc": 1, "hs": hs, "dtype": dtype}, call="hcgr_block_norm_bwd",
+                   args=[x, hs, w, rr, d, M, dx, dw, ws, ws_bytes], **q)
 
 
 def linear(rec, M, n, k, dtype=H.HCGR_BF16, ld_out=None, shift=0, **q):
@@ -132,3 +141,29 @@ def test_calls_run_on_the_handle_s_device(rec, call, current):
         a = CALLS[call](rec, device=device, current=current, stream=(1 - device) * 16 + 3)
         assert a["status"] == H.HCGR_ERR_INVALID_ARGUMENT and "stream belongs to" in a["error"]
         assert not a["launches"] and a["current"] == current
+
+
+def test_every_kernel_is_run_by_a_gpu_test(rec):
+    """The shapes of the GPU tests reach every kernel of these operators that
+    the library holds, so that a changed rule of choice leaves none untested."""
+    import test_gpu_block as G
+
+    def name(kernel):
+        return re.sub(r"hcgr::|\(anonymous namespace\)::|^void ", "", kernel).split("(")[0]
+
+    asked = []
+    for dtype in BYTES:
+        for hs, m in G.SHAPES + G.OTHER_NORM:
+            asked += [norm(rec, m, hs, dtype), norm_backward(rec, m, hs, dtype)]
+        for hs, m in G.OTHER_NORM:
+            asked.append(quantize(rec, m, hs, dtype))
+        for hc, hs, m in G.RES_SHAPES + G.OTHER_RES:
+            asked += [residual(rec, m, hs, hc, dtype), backward(rec, m, hs, hc, dtype)]
+        for k, m in next(p.args[1] for p in G.test_quantize.pytestmark if p.args[:1] == ("k,m",)):
+            asked.append(quantize(rec, m, k, dtype))
+        for n, k, m in G.LIN + G.OTHER_LIN:
+            asked.append(linear(rec, m, n, k, dtype))
+    run = {name(la["kernel"]) for a in asked for la in check_sizes(a)}
+    held = {name(k) for k in rec.kernels()}
+    held = {k for k in held if k.startswith(("norm_", "linear_"))}
+    assert len(held) > 150 and not held - run, sorted(held - run)

@@ -209,6 +209,29 @@ def test_plain_combine_is_the_op_s_combine(H):
     assert float((d > 0).float().mean()) < 1e-3
 
 
+# Shapes of the kernels that the lists above do not reach (test_block_launches.py
+# checks that every kernel is reached): wide rows of odd widths, by passes or two
+# pieces a thread, and wide rows of one and two streams.
+OTHER_NORM = [(1001, 9), (2563, 5), (4096, 6), (8187, 4), (8192, 5), (9001, 3), (16383, 3), (24577, 3), (65535, 2)]
+OTHER_RES = [(8, 1001, 6), (8, 2563, 3), (4, 2563, 5), (4, 8187, 3), (1, 2563, 40), (1, 8192, 5), (2, 8192, 5),
+             (2, 4096, 7), (1, 16384, 2), (2, 16384, 3), (1, 8187, 3), (2, 24577, 2), (4, 9001, 2)]
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("hs,m", OTHER_NORM)
+def test_norm_of_other_widths(H, hs, m, dt):
+    test_norm(H, hs, m, dt)
+    test_norm_bwd(H, hs, m, dt)
+    test_quantize(H, hs, m, dt)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("hc,hs,m", OTHER_RES)
+def test_residual_of_other_widths(H, hc, hs, m, dt):
+    test_residual(H, hc, hs, m, dt)
+    test_residual_bwd(H, hc, hs, m, dt)
+
+
 # ------------------------------------------------- strides, streams, graphs --
 @pytest.mark.parametrize("hs,off", [(2560, 0), (2560, 1), (1000, 8), (129, 0)])
 def test_strided_and_unaligned_rows(H, hs, off):
@@ -398,6 +421,38 @@ def test_linear(H, n, k, m, dt):
         # the sum is exact; its conversion, the scales' product, the product
         # and the addition round once each: four roundings
         B.check(out, B.linear(**i), "out", 4)
+
+
+# Shapes of the kernels that LIN does not reach: tiles of outputs that are not
+# whole pieces of four, 64 x 64 with a ragged K and N, few tokens with more than
+# 4096 channels, streaming stores from 128-token tiles, and 256-token tiles of
+# fp32 results that the caches hold.
+OTHER_LIN = [(2501, 640, 513), (777, 1000, 2000), (2501, 640, 4000), (8191, 513, 3000), (1023, 513, 1023),
+             (777, 1000, 1000), (10240, 2560, 32), (10237, 2561, 20), (5000, 2560, 8), (5003, 2570, 24),
+             (2560, 64, 8192), (32772, 640, 129)]
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("n,k,m", OTHER_LIN)
+def test_linear_of_other_shapes(H, n, k, m, dt):
+    test_linear(H, n, k, m, dt)
+
+
+@pytest.mark.parametrize("n,k,m", [(2500, 640, 513), (2501, 640, 4000), (5000, 100, 3000), (1024, 512, 1023), (10240, 2560, 20)])
+@pytest.mark.parametrize("off", [0, 1, 4])
+def test_linear_strided_outputs_of_tiles(H, n, k, m, off):
+    """Outputs inside a wider tensor, at a start that is and is not a whole
+    piece of four: the bits of a dense output, and nothing around it."""
+    say("strided tiles", n, k, m, off)
+    lin = H.Int8Linear(H.LinearConfig(n=n, k=k), 0)
+    i = linear_inputs(gen(n + off), n, k, m, BF16)
+    want = lin.forward(**i)
+    for pad in (5, 8):
+        around = torch.full((m + 1, n + pad), 9.0, dtype=BF16, device="cuda")
+        lin.forward(**i, out=around[:m, off:off + n])
+        assert torch.equal(around[:m, off:off + n], want)
+        assert bool((around[:m, :off] == 9).all()) and bool((around[:m, off + n:] == 9).all())
+        assert bool((around[m] == 9).all())
 
 
 def test_linear_largest_sums(H):
