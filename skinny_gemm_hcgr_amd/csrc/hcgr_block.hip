@@ -722,10 +722,14 @@ __global__ __launch_bounds__(1024) void norm_row(NormArgs a) {
 // One-wave rows: four rows at a time, the four waves' sums meet in LDS. Up to
 // 512 threads the next row's pieces come to LDS behind this row's products and
 // stores, each wave's into a place of its own (no barrier). At M = 8192, HC =
-// 4, HS = 2560 the pass takes 158 us (4.0 TB/s; 5.2 TB/s, what a copy reaches,
-// would take 121): 194 us with the loads of a row waiting for the row before,
-// 169 with the next row ahead, 162 with three workgroups a CU (128 registers)
-// in place of two, the rest by streaming stores.
+// 4, HS = 2560, bf16, the call takes 156 us with norm_bwd_sum (4.0 TB/s; 5.2
+// TB/s, what a copy reaches, would take 121): 194 us with the loads of a row
+// waiting for the row before, 169 with the next row ahead, 162 with three
+// workgroups a CU (128 registers) in place of two, 158 by streaming stores, 156
+// with the gates formed before the next row's loads (the compiler's wait for the
+// logits took those in). fp16 takes 148. What bounds it: 128 registers do not
+// hold four streams in 16 bits; 3 are spilled, and a reload waits for every load
+// in flight, the next row's among them, before the reduction.
 // ---------------------------------------------------------------------------
 constexpr int bwd_loads(int hc) { return hc ? 2 * hc + 2 : 2; }  // hc = 0: the norm alone
 // Dynamic LDS of norm_bwd_row: the waves' places, and room for the sums of

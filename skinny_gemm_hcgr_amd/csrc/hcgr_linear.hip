@@ -218,8 +218,9 @@ __global__ __launch_bounds__(512) void linear_split(LinearArgs a, int rows, int 
 // into the next tile, so that its first stages arrive behind this one's
 // epilogue. Past the last tile they are out of range and bring zeros. A tile's
 // scales come the same way. The epilogue turns the sums around in the one free
-// ring buffer, so that stores are whole 128-byte lines and nothing in it waits
-// for memory.
+// ring buffer, so that stores are whole 128-byte lines; without a bias nothing
+// in it waits for memory. A bias is loaded there and waited for, with all that
+// is in flight (8192x10240x2560: 216 us without, 218 with).
 // ---------------------------------------------------------------------------
 typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
 template <int TM, int TN>
