@@ -2113,15 +2113,27 @@ int launch_combine(const CombineArgs& args, void* stream) {
   // streaming policy once R2 outgrows the L2s (8 x 4 MB): 73% -> 81% of HBM
   // peak at M = 8192 (HC = 4, HS = 2560) on MI355X
   a.nt = (double)a.M * a.HC * a.HS * 2.0 > 32.0 * 1024 * 1024 ? 1 : 0;
-  const int64_t groups = cdiv(a.M, 8) * 8 * a.HC;  // token octets x streams x 8
   const int passes = (int)cdiv(a.HS / 8, kCombineThreads);  // chunks per thread in one pass
-  const dim3 g((unsigned)groups), blk(kCombineThreads);
+  const dim3 blk(kCombineThreads);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (passes <= 1) hipLaunchKernelGGL(hcgr_combine_k<1>, g, blk, 0, st, a);
-  else if (passes <= 2) hipLaunchKernelGGL(hcgr_combine_k<2>, g, blk, 0, st, a);
-  else if (passes <= 4) hipLaunchKernelGGL(hcgr_combine_k<4>, g, blk, 0, st, a);
-  else hipLaunchKernelGGL(hcgr_combine_k<8>, g, blk, 0, st, a);
-  return (int)hipGetLastError();
+  // HIP takes fewer than 2^32 threads in a dimension: 2^31 a launch, longer
+  // calls in several
+  const int64_t rows = ((int64_t)1 << 31) / (kCombineThreads * a.HC);
+  for (int64_t m0 = 0; m0 < args.M; m0 += rows) {
+    a.R = args.R + m0 * a.HC * a.HS;
+    a.y = args.y + m0 * a.HS;
+    a.inj = args.inj + m0 * a.ld_inj;
+    a.R2 = args.R2 + m0 * a.HC * a.HS;
+    a.M = args.M - m0 < rows ? args.M - m0 : rows;
+    const dim3 g((unsigned)(cdiv(a.M, 8) * 8 * a.HC));  // token octets x streams x 8
+    if (passes <= 1) hipLaunchKernelGGL(hcgr_combine_k<1>, g, blk, 0, st, a);
+    else if (passes <= 2) hipLaunchKernelGGL(hcgr_combine_k<2>, g, blk, 0, st, a);
+    else if (passes <= 4) hipLaunchKernelGGL(hcgr_combine_k<4>, g, blk, 0, st, a);
+    else hipLaunchKernelGGL(hcgr_combine_k<8>, g, blk, 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+  }
+  return (int)hipSuccess;
 }
 
 // ---------------------------------------------------------------------------

@@ -122,6 +122,21 @@ def test_other_launches_of_the_longest_calls(rec, hs, hc, dtype):
         check_sizes(linear(rec, M, hs, 16, dtype))
 
 
+def combine(rec, M, hs, hc, **q):
+    R, y, inj, R2 = places(M * hc * hs * 2, M * hs * 2, M * hc * 2, M * hc * hs * 2)
+    return rec.ask(config="Config", values={"hc": hc, "hs": hs, "r": 32}, call="hcgr_combine",
+                   args=[R, y, inj, hc, M, R2], **q)
+
+
+@pytest.mark.parametrize("hs,hc", [(128, 1), (128, 4), (2560, 4), (8192, 8)])
+def test_combine_launches_of_the_longest_calls(rec, hs, hc):
+    edge = (1 << 32) // (256 * hc)  # a workgroup of 256 a token and stream
+    for M in (1, edge - 8, edge, edge + 1, 4 * edge + 5):
+        launches = check_sizes(combine(rec, M, hs, hc))
+        groups = sum(la["gx"] for la in launches)
+        assert M * hc <= groups < (M + 8) * hc, (M, launches)
+
+
 CALLS = {"norm": lambda rec, **q: norm(rec, 100, 2560, **q), "residual": lambda rec, **q: residual(rec, 100, 512, 4, **q),
          "quantize": lambda rec, **q: quantize(rec, 100, 777, **q), "backward": lambda rec, **q: backward(rec, 100, 512, 4, **q),
          "linear": lambda rec, **q: linear(rec, 100, 2560, 512, **q)}

@@ -843,3 +843,21 @@ def test_more_rows_than_one_launch_takes(H):
     ref = B.norm(x[rows], w, EPS)
     B.check(out["x"][rows], ref["x"], "x")
     B.check(out["rrms"][rows], ref["rrms"], "rrms")
+
+
+def test_combine_of_more_tokens_than_one_launch_takes(H):
+    """Past 2^22 tokens of four streams a launch of the op's combine would pass
+    2^32 threads."""
+    m, hc, hs = (1 << 22) + 37, 4, 128
+    say("many tokens", m)
+    op, g = H.HCGR(H.Config(hc=hc, hs=hs, r=32), 0), gen(23)
+    R = torch.empty((m, hc * hs), dtype=BF16, device="cuda")
+    for a in range(0, m, 1 << 20):
+        R[a:a + (1 << 20)] = randn(g, min(1 << 20, m - a), hc * hs, dtype=BF16)
+    y, inj = randn(g, m, hs, dtype=BF16), randn(g, m, hc, dtype=BF16)
+    R2 = torch.full_like(R, float("nan"))
+    op.combine(R, y, inj, R2=R2)
+    assert not bool(R2.isnan().any())
+    rows = torch.tensor([r + d for r in (0, 1 << 21, 1 << 22, m) for d in range(-9, 9) if 0 <= r + d < m], device="cuda")
+    ref = B.residual(R[rows], y[rows], inj[rows], None, None, hc=hc, eps=EPS, rho=1.0)
+    B.check(R2[rows], ref["R2"], "R2")
