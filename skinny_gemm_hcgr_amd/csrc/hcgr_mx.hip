@@ -141,7 +141,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 // 64 channels' bias to LDS, a value in each 32-bit word (zero past `bytes`): asked
 // for ahead of the products, as its latency would stand behind them (1024 x 10240 x
-// 2560: 24.8 us with a bias, 22.4 without; 20.9 both ways by way of LDS).
+// 2560: 2.4 us; by way of LDS 0.6).
 template <int DT>
 __device__ __forceinline__ void load_bias(const void* bias, int n0, int channels, int lane, uint32_t lds) {
   constexpr int B = DT == 2 ? 4 : 2;
@@ -358,7 +358,7 @@ int launch_split(const MxLinearArgs& a, int nw, hipStream_t st) {
 // ---------------------------------------------------------------------------
 constexpr int kTurn = 2048;  // a wave's LDS in the epilogue: 16 rows of 128 bytes
 template <int TM, int TN, int NW>
-constexpr int tile_lds() { return (TM + TN) * (2 * 128 + 16) + NW * kTurn + 2 * TN * 4; }
+constexpr int tile_lds() { return (TM + TN) * (2 * 128 + 16) + NW * kTurn + 3 * TN * 4; }
 template <int TM, int TN, int NW>
 constexpr int tile_groups() { return 160 * 1024 / tile_lds<TM, TN, NW>(); }  // workgroups a CU
 
@@ -489,7 +489,7 @@ __global__ __launch_bounds__(64 * NW, (tile_groups<TM, TN, NW>() * NW / 4)) void
       scale[f][1] = __builtin_amdgcn_perm(raw[f].w & keep(3), raw[f].z & keep(2), pick);
     }
   };
-  f32x16_t acc[FN][FM], start[FN];  // start: a tile's bias
+  f32x16_t acc[FN][FM];
   // Unit u, the POS-th of its group, in buffer POS. Its first step's fragments
   // are in registers, and in POS 0 its group's scales. FIRST: of its tile.
   auto unit = [&](int u, auto POS, auto FIRST) {
@@ -502,7 +502,7 @@ __global__ __launch_bounds__(64 * NW, (tile_groups<TM, TN, NW>() * NW / 4)) void
       each<NM>([&](auto T) {
         constexpr int t = decltype(T)::value, f = t / FM, g = t % FM;
         acc[f][g] = mfma_mx32<st, st>(frag[st % 2][f], frag[st % 2][FN + g],
-                                      decltype(FIRST)::value && st == 0 ? start[f] : acc[f][g], scale[f][pos], scale[FN + g][pos]);
+                                      decltype(FIRST)::value && st == 0 ? f32x16_t{} : acc[f][g], scale[f][pos], scale[FN + g][pos]);
         after(T);
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -551,12 +551,14 @@ __global__ __launch_bounds__(64 * NW, (tile_groups<TM, TN, NW>() * NW / 4)) void
     products(ic<3>{}, [&](auto T) { behind(ic<NM + decltype(T)::value>{}); });
   };
 
-  // A tile's bias comes with the tile before, in two places in turn.
+  // A tile's bias comes with the tile before, in three places in turn: it is
+  // read at the tile's end, when a wave that is ahead asks for that of the tile
+  // after the next.
   constexpr int kBias = 2 * UB + (TM + TN) * 16 + NW * kTurn;
   auto bias_of = [&](const Aim& z, int j) {
     if (a.bias && wave * 64 < TN)
       load_bias<DT>(a.bias, z.n0 + wave * 64, min(z.channels - wave * 64, 64), lane,
-                    lds0 + (uint32_t)(kBias + j % 2 * (TN * 4) + wave * 256));
+                    lds0 + (uint32_t)(kBias + j % 3 * (TN * 4) + wave * 256));
   };
   bias_of(now, 0);
   load_scales();
@@ -571,26 +573,29 @@ __global__ __launch_bounds__(64 * NW, (tile_groups<TM, TN, NW>() * NW / 4)) void
   int m0 = 0, n0 = 0;
   for (int j = 0; place(j, m0, n0); ++j) {
     const int el = hidden(lane), col = wn * (32 * FN), mr = min(TM, (int)a.M - m0), nr = min(TN, a.n - n0);
-    // Sums: lane -> token lane % 32, channels 8*(i/4) + 4*(lane/32) + i % 4.
-#pragma unroll
-    for (int f = 0; f < FN; ++f) start[f] = f32x16_t{};
+    bias_of(next, j + 1);
+    unit(0, ic<0>{}, ic<1>{});
+    unit(1, ic<1>{}, ic<0>{});
+    for (int u = 2; u < units; u += 2) {
+      unit(u, ic<0>{}, ic<0>{});
+      unit(u + 1, ic<1>{}, ic<0>{});
+    }
+    // Sums: lane -> token lane % 32, channels 8*(i/4) + 4*(lane/32) + i % 4. The
+    // bias joins the whole sum: at the start of the accumulators each of K/64
+    // additions would round at its size (and 8192 x 10240 x 2560 take 112.4 us for
+    // 113.7).
     if (a.bias) {
 #pragma unroll
       for (int f = 0; f < FN; ++f)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float bias[4];
-          bias4<DT>(lds + kBias + j % 2 * (TN * 4) + (col + f * 32 + q * 8 + el / 32 * 4) * 4, bias);
+          bias4<DT>(lds + kBias + j % 3 * (TN * 4) + (col + f * 32 + q * 8 + el / 32 * 4) * 4, bias);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) start[f][q * 4 + i] = bias[i];
+          for (int g = 0; g < FM; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[f][g][q * 4 + i] += bias[i];
         }
-      bias_of(next, j + 1);
-    }
-    unit(0, ic<0>{}, ic<1>{});
-    unit(1, ic<1>{}, ic<0>{});
-    for (int u = 2; u < units; u += 2) {
-      unit(u, ic<0>{}, ic<0>{});
-      unit(u + 1, ic<1>{}, ic<0>{});
     }
     if constexpr (VEC) {
       // Rounded, and through the wave's 2 KB of LDS, so that a store is whole
