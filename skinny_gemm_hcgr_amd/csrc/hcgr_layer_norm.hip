@@ -22,6 +22,10 @@ namespace {
 //   var  = sum_w (S2 + 2 c S1 + n c^2) / HS,  c = a - mean = (a - A) - D,
 // and a value's distance from the mean is (x - a) + c: the mean is never
 // rounded to one number where it is large next to the deviations.
+//
+// A row gives the same bits whatever batch it stands in: how its sums are cut
+// and joined is a function of its width alone. Where few rows take more waves
+// than many do (whole_row), they add up what one wave would, in its order.
 // ---------------------------------------------------------------------------
 struct Spread {
   float mean, rstd, c;  // c: what a value's distance from its wave's mean lacks
@@ -36,18 +40,34 @@ __device__ __forceinline__ int values_of_wave(int wave, int threads, int nch, in
   for (int j = 0; j < nch; ++j) n += min(max(hs - (j * threads + wave * 64) * V, 0), 64 * V);
   return n;
 }
-// `red`: three floats a wave.
+// A lane's N sums over its pieces of the whole row, of which each wave has one
+// piece a lane: in the order of the pieces, as one wave that holds all of them
+// adds. `red`: 64*N floats a wave.
+template <int N>
+__device__ __forceinline__ void whole_row(float (&v)[N], float* red) {
+  const int nw = (int)blockDim.x / 64, w = (int)threadIdx.x / 64, lane = (int)threadIdx.x % 64;
+  if (nw == 1) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) red[(w * N + i) * 64 + lane] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = red[i * 64 + lane];
+  for (int k = 1; k < nw; ++k) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += red[(k * N + i) * 64 + lane];
+  }
+}
+// The statistics of a row from the sums over all of it.
+__device__ __forceinline__ Spread spread_of_row(float a, float s1, float s2, int hs, float eps) {
+  const float d = s1 / (float)hs;
+  return {a + d, rstd_of(fmaf(-d, d, s2 / (float)hs), eps), -d};
+}
+// And from those of its waves. `red`: three floats a wave.
 template <int V>
 __device__ __forceinline__ Spread spread_of(float a, float s1, float s2, int nch, int hs, float eps, float* red) {
   const int nw = (int)blockDim.x / 64, w = (int)threadIdx.x / 64;
+  if (nw == 1) return spread_of_row(a, s1, s2, hs, eps);
   Spread z;
-  if (nw == 1) {
-    const float d = s1 / (float)hs;
-    z.mean = a + d;
-    z.rstd = rstd_of(fmaf(-d, d, s2 / (float)hs), eps);
-    z.c = -d;
-    return z;
-  }
   if (threadIdx.x % 64 == 0) {
     red[w * 3] = a;
     red[w * 3 + 1] = s1;
@@ -89,12 +109,14 @@ __device__ __forceinline__ void affine(float (&d)[V], float add, float r, bool h
 // ---------------------------------------------------------------------------
 // layer_norm_row: rows that fit the registers of a workgroup (NCH 16-byte
 // pieces a thread): each value is read once. Rows of at most 64 * NCH pieces
-// take one wave, four rows a workgroup, without barriers.
+// take one wave, four rows a workgroup, without barriers. With one piece a
+// thread the waves (up to kWholeWaves) sum as one wave would.
 // ---------------------------------------------------------------------------
+constexpr int kWholeWaves = 5;
 template <typename T, int NCH, bool AL>
 __global__ __launch_bounds__(1024) void layer_norm_row(LayerNormArgs a) {
   constexpr int V = vec<T>();
-  __shared__ float red[16 * 3];
+  __shared__ float red[NCH == 1 ? kWholeWaves * 64 * 3 : 16 * 3];
   const int hs = a.hs, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
   const int64_t m = a.m_first + (int64_t)blockIdx.x * blockDim.y + __builtin_amdgcn_readfirstlane((int)threadIdx.y);
   if (m >= a.M) return;  // blockDim.y > 1 only without barriers
@@ -106,26 +128,39 @@ __global__ __launch_bounds__(1024) void layer_norm_row(LayerNormArgs a) {
     wr[j] = rw.get(j);
     br[j] = rb.get(j);
   }
-  float d[NCH][V], s = 0.0f;
+  // From three pieces a thread on, whose rows one wave or several may hold: sums
+  // of each piece, then of the pieces in turn. Otherwise in one go (1000 fp16
+  // channels, 1024 rows: 3.2 us for 3.3).
+  constexpr bool APART = NCH >= 3;
+  float d[NCH][V], s[1] = {};
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
     unpack<T>(xr[j], d[j]);
+    float p = APART ? 0.0f : s[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += d[j][i];
+    for (int i = 0; i < V; ++i) p += d[j][i];
+    s[0] = APART && j > 0 ? s[0] + p : p;
   }
-  const float mine = wave_sum(s) / (float)values_of_wave<V>(wave, (int)blockDim.x, NCH, hs);
-  float s1 = 0.0f, s2 = 0.0f;
+  if constexpr (NCH == 1) whole_row(s, red);
+  const int values = NCH == 1 ? hs : values_of_wave<V>(wave, (int)blockDim.x, NCH, hs);
+  const float mine = wave_sum(s[0]) / (float)values;
+  float dev[2] = {};
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
     const int n = hs - ((int)threadIdx.x + j * (int)blockDim.x) * V;
+    float p1 = APART ? 0.0f : dev[0], p2 = APART ? 0.0f : dev[1];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       d[j][i] = (AL ? n > 0 : i < n) ? d[j][i] - mine : 0.0f;
-      s1 += d[j][i];
-      s2 += d[j][i] * d[j][i];
+      p1 += d[j][i];
+      p2 = fmaf(d[j][i], d[j][i], p2);
     }
+    dev[0] = APART && j > 0 ? dev[0] + p1 : p1;
+    dev[1] = APART && j > 0 ? dev[1] + p2 : p2;
   }
-  const Spread z = spread_of<V>(mine, wave_sum(s1), wave_sum(s2), NCH, hs, a.eps, red);
+  if constexpr (NCH == 1) whole_row(dev, red + kWholeWaves * 64);
+  const float s1 = wave_sum(dev[0]), s2 = wave_sum(dev[1]);
+  const Spread z = NCH == 1 ? spread_of_row(mine, s1, s2, hs, a.eps) : spread_of<V>(mine, s1, s2, NCH, hs, a.eps, red);
   if (a.stats && threadIdx.x == 0) {
     a.stats[2 * m] = z.mean;
     a.stats[2 * m + 1] = z.rstd;
@@ -477,17 +512,23 @@ int forward_loop(const LayerNormArgs& a, hipStream_t st) {
 // A row by as few waves as its registers allow, so that the reductions and the
 // statistics are not repeated wave by wave (16384 rows of 2560 bf16 channels by
 // one wave 27 us, 6.2 TB/s, by five 43 us; 512 rows of 8192 channels by four
-// 6.0 us, by eight 8.0), but by 64 pieces a wave where neither rows nor width
-// give the CUs work (one row of 2560 channels by five waves 3.2 us, by one 3.3;
-// 512 rows 3.9 and 4.0, 768 rows 4.5 and 4.2; one row of 4096 3.0 and 3.6).
+// 6.0 us, by eight 8.0). Few rows of 129 to 320 pieces leave CUs idle and go by
+// one piece a thread, with the same bits (one row of 2560 channels 3.0 us, by one
+// wave 3.4; 512 rows 3.9 and 4.0, 1024 rows 5.3 and 4.5; off 16 bytes one row of
+// 2555 3.7 and 5.0, 1024 rows 5.8 and 6.2). Rows of 321 to 640 pieces go by two a
+// thread, which serves few and many (4096 channels by one, two, four pieces: one
+// row 3.1, 3.2, 3.6 us, 512 rows 4.5, 4.2, 4.8, 16384 rows 68, 50, 49; 5120 by five:
+// one row 3.9 for 3.5, 16384 rows 62 for 67).
 template <typename T, bool AL>
 int forward_al(const LayerNormArgs& a, hipStream_t st) {
   const int64_t pieces = cdiv64(a.hs, vec<T>());
   if (pieces > 2048) return forward_loop<T, AL>(a, st);
-  if (pieces <= 64 || (a.M < 640 && pieces > 128 && pieces <= 640)) return forward_row<T, 1, AL>(a, st);
+  if (pieces <= 64 || (a.M < 640 && pieces > 128 && pieces <= 64 * kWholeWaves)) return forward_row<T, 1, AL>(a, st);
   if (pieces <= 128) return forward_row<T, 2, AL>(a, st);
   if (pieces <= 192) return forward_row<T, 3, AL>(a, st);
-  if (pieces > 256 && pieces <= 320) return forward_row<T, 5, AL>(a, st);
+  if (pieces <= 256) return forward_row<T, 4, AL>(a, st);
+  if (pieces <= 320) return forward_row<T, 5, AL>(a, st);
+  if (pieces <= 640) return forward_row<T, 2, AL>(a, st);
   return forward_row<T, 4, AL>(a, st);
 }
 template <typename T>

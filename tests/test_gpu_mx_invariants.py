@@ -30,3 +30,32 @@ def test_bias_joins_the_whole_sum(H, n, k, m):  # noqa: F811
     i["bias"] = randn(gen(m), n, scale=2.0 ** 20)
     val, amp = X.linear(i["q"], i["q_scale"], i["w"], i["w_scale"], None, k)
     B.check(lin.forward(**i), (val + i["bias"].double(), amp), "out", X.c_of(k))
+
+
+# Pieces of 16 bytes a row: every layout of the norm's forward pass, at and beside the widths where it changes.
+WIDTHS = [3, 64, 65, 128, 129, 192, 193, 256, 257, 320, 321, 500, 640, 641, 1030, 2048, 2050]
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32], ids=str)
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("pieces", WIDTHS)
+def test_a_norm_s_bits_do_not_depend_on_the_batch(H, pieces, odd, dt):  # noqa: F811
+    """A row alone, among few, and among many: the same statistics, norm, codes
+    and scales; and the same gradient of the row."""
+    hs, m = pieces * (16 // dt.itemsize) - (1 if odd else 0), 700
+    say("batches", hs, dt)
+    blk, g = H.Block(H.BlockConfig(hc=1, hs=hs, dtype=H.HCGR_BF16 if dt is BF16 else H.HCGR_FP32), 0), gen(hs)
+    x = (randn(g, m, hs, scale=3.0) + randn(g, m, 1, scale=8.0)).to(dt)
+    w, b, d = randn(g, hs, dtype=dt), randn(g, hs, dtype=dt), randn(g, m, hs, dtype=dt)
+
+    def both(rows):
+        return blk.layer_norm(x[rows], w, b, out=blk.alloc_layer_norm(len(x[rows]), quantize=True, keep=True))
+
+    full = both(slice(0, m))
+    dx = blk.layer_norm_bwd(x, w, full["stats"], d)["dx"]
+    for rows in (slice(0, 1), slice(17, 30), slice(30, 669), slice(60, 700), slice(699, 700)):
+        part = both(rows)
+        for name in part:
+            assert torch.equal(part[name], full[name][rows]), (name, rows)
+        got = blk.layer_norm_bwd(x[rows], w, part["stats"], d[rows])["dx"]
+        assert torch.equal(got, dx[rows]), rows
