@@ -490,17 +490,20 @@ hcgr_status hcgr_block_residual_bwd(hcgr_block_handle h, const void* R, const vo
  *                       them), or NULL
  * At least one of xn and q is given. The deviations are taken from a mean that
  * is held in more than 32 bits, so that a mean far from zero costs no digits. A
- * row that holds an infinity or a NaN gives NaN. Errors as hcgr_block_norm. */
+ * row that holds an infinity or a NaN gives NaN. A row's bits depend on HS and on
+ * whether the call's rows are aligned (see above), not on M. Errors as
+ * hcgr_block_norm. */
 hcgr_status hcgr_block_layer_norm(hcgr_block_handle h, const void* x, int64_t ld_x, const void* w, const void* b,
                                   int64_t M, void* xn, uint8_t* q, int64_t ld_q, uint8_t* q_scale, int64_t ld_qs,
                                   float* stats, void* stream);
 
 /* Gradients of xn = layer_norm(x, w, b): with h = (x - mean)*r, e = dxn*w,
  *   dx = r*(e - mean_c(e) - h*mean_c(e*h)),  dw = sum_m dxn*h,  db = sum_m dxn.
- *   stats [M, 2] float, from hcgr_block_layer_norm on the same x; dxn [M, HS]
- *   dtype; w as there (NULL: 1); dx [M, HS] dtype or NULL; dw, db [HS] float
- *   (summed over the M tokens; written, not added to) or NULL; at least one of
- *   the three is given.
+ *   stats [M, 2] float, from hcgr_block_layer_norm on the same x; they enter as
+ *   they are, the mean rounded to 32 bits (fp32 rows whose mean lies D deviations
+ *   from zero have an h that is off by up to D * 2^-24); dxn [M, HS] dtype; w as
+ *   there (NULL: 1); dx [M, HS] dtype or NULL; dw, db [HS] float (summed over the M
+ *   tokens; written, not added to) or NULL; at least one of the three is given.
  * Workspace and errors as hcgr_block_norm_bwd; with M == 0 dw and db are not
  * written. */
 hcgr_status hcgr_block_layer_norm_bwd(hcgr_block_handle h, const void* x, int64_t ld_x, const void* w,
