@@ -44,7 +44,10 @@ int launch_norm(const NormArgs& a, int dtype, bool residual, void* stream);
 int launch_norm_bwd(const NormBwdArgs& a, int dtype, bool residual, void* stream);
 // Rows -> int8 rows and a scale each: launch_norm without the norm.
 int launch_quantize(const NormArgs& a, int dtype, void* stream);
-int configure_block_kernels();
+// configure_*: raise the dynamic-LDS limits of the kernels that a handle of this
+// type (and width) may launch, on the current device. Each costs some 50 ns,
+// the first of a source's kernels in a process the load of its code (1 to 3 ms).
+int configure_block_kernels(int dtype);
 // The workspace of every norm's backward pass: two floats a row, then up to
 // norm_bwd_groups(M) pairs of partial sums [2][HS] of the weight gradients.
 size_t norm_bwd_workspace(int hs, int64_t M);
@@ -78,7 +81,7 @@ struct LayerNormBwdArgs {
 };
 int launch_layer_norm(const LayerNormArgs& a, int dtype, void* stream);
 int launch_layer_norm_bwd(const LayerNormBwdArgs& a, int dtype, void* stream);
-int configure_layer_norm_kernels();
+int configure_layer_norm_kernels(int hs, int dtype);
 
 struct LinearArgs {
   const int8_t *q, *w;
@@ -89,7 +92,7 @@ struct LinearArgs {
   int n, k;
 };
 int launch_linear(const LinearArgs& a, int dtype, void* stream);
-int configure_linear_kernels();
+int configure_linear_kernels(int dtype);
 
 // Rows to microscaled 4 bits, and back.
 template <typename X, typename Q>
@@ -111,6 +114,6 @@ struct MxLinearArgs {
 int launch_mx_quantize(const MxRowsToArgs& a, int dtype, void* stream);
 int launch_mx_dequantize(const MxRowsFromArgs& a, int dtype, void* stream);
 int launch_mx_linear(const MxLinearArgs& a, int dtype, void* stream);
-int configure_mx_kernels();
+int configure_mx_kernels(int dtype);
 
 }  // namespace hcgr

@@ -979,11 +979,8 @@ int launch_norm_bwd(const NormBwdArgs& a, int dtype, bool residual, void* stream
                       : backward_of<Fp32>(a, residual, st);
 }
 
-// Raises the dynamic-LDS limit of the backward kernels on the current device.
-int configure_block_kernels() {
-  for (const hipError_t e : {raise_lds<Bf16>(), raise_lds<Fp16>(), raise_lds<Fp32>()})
-    if (e != hipSuccess) return (int)e;
-  return (int)hipSuccess;
+int configure_block_kernels(int dtype) {
+  return (int)(dtype == 0 ? raise_lds<Bf16>() : dtype == 1 ? raise_lds<Fp16>() : raise_lds<Fp32>());
 }
 
 size_t norm_bwd_workspace(int hs, int64_t M) {

@@ -397,7 +397,8 @@ hcgr_status on_device(int device, void* stream, F launch) {
 }
 
 // Sets the kernels' attributes on `device`.
-hcgr_status configure(int device, int (*set)()) {
+template <typename F>
+hcgr_status configure(int device, F set) {
   int cur = -1;
   hipError_t e = hipGetDevice(&cur);
   if (e != hipSuccess) return fail(HCGR_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(e));
@@ -420,8 +421,11 @@ hcgr_status hcgr_block_create(const hcgr_block_config* cfg, int device, hcgr_blo
   hcgr_status st = check_block(cfg);
   if (st != HCGR_OK) return st;
   if ((st = check_device(device)) != HCGR_OK) return st;
-  if ((st = configure(device, hcgr::configure_block_kernels)) != HCGR_OK) return st;
-  if ((st = configure(device, hcgr::configure_layer_norm_kernels)) != HCGR_OK) return st;
+  st = configure(device, [&] {
+    const int e = hcgr::configure_block_kernels(cfg->dtype);
+    return e != (int)hipSuccess ? e : hcgr::configure_layer_norm_kernels(cfg->hs, cfg->dtype);
+  });
+  if (st != HCGR_OK) return st;
   hcgr_block_op* op = new (std::nothrow) hcgr_block_op;
   if (!op) return fail(HCGR_ERR_INVALID_ARGUMENT, "out of host memory");
   op->cfg = *cfg;
@@ -610,8 +614,11 @@ hcgr_status hcgr_linear_create(const hcgr_linear_config* cfg, int device, hcgr_l
   hcgr_status st = check_linear(cfg);
   if (st != HCGR_OK) return st;
   if ((st = check_device(device)) != HCGR_OK) return st;
-  if ((st = configure(device, hcgr::configure_linear_kernels)) != HCGR_OK) return st;
-  if ((st = configure(device, hcgr::configure_mx_kernels)) != HCGR_OK) return st;
+  st = configure(device, [&] {
+    const int e = hcgr::configure_linear_kernels(cfg->dtype);
+    return e != (int)hipSuccess ? e : hcgr::configure_mx_kernels(cfg->dtype);
+  });
+  if (st != HCGR_OK) return st;
   hcgr_linear_op* op = new (std::nothrow) hcgr_linear_op;
   if (!op) return fail(HCGR_ERR_INVALID_ARGUMENT, "out of host memory");
   op->cfg = *cfg;

@@ -563,33 +563,48 @@ int backward_loop(const LayerNormBwdArgs& a, hipStream_t st) {
                      dim3(kBwdColThreads), 0, st, a);
   return launch_weight_sums(a.part, a.hs, groups, a.dw, a.db, st);
 }
+// Pieces a thread of layer_norm_bwd_row for a row of that many; 0: the kernels
+// for any width.
+int bwd_pieces(int64_t pieces) {
+  if (pieces <= 64) return 1;
+  if (pieces <= 128) return 2;
+  // five where they leave fewer threads idle than four (2560 channels: 320 or
+  // 640 pieces)
+  if (pieces <= 2048) return cdiv64(pieces, 320) * 320 < cdiv64(pieces, 256) * 256 ? 5 : 4;
+  return 0;
+}
 template <typename T, bool AL>
 int backward_al(const LayerNormBwdArgs& a, hipStream_t st) {
-  const int64_t pieces = cdiv64(a.hs, vec<T>());
-  if (pieces <= 64) return backward_row<T, 1, AL>(a, st);
-  if (pieces <= 128) return backward_row<T, 2, AL>(a, st);
-  // five pieces a thread where they leave fewer threads idle than four (2560
-  // channels: 320 or 640 pieces)
-  if (pieces <= 2048 && cdiv64(pieces, 320) * 320 < cdiv64(pieces, 256) * 256) return backward_row<T, 5, AL>(a, st);
-  if (pieces <= 2048) return backward_row<T, 4, AL>(a, st);
-  return backward_loop<T, AL>(a, st);
+  switch (bwd_pieces(cdiv64(a.hs, vec<T>()))) {
+    case 1: return backward_row<T, 1, AL>(a, st);
+    case 2: return backward_row<T, 2, AL>(a, st);
+    case 4: return backward_row<T, 4, AL>(a, st);
+    case 5: return backward_row<T, 5, AL>(a, st);
+    default: return backward_loop<T, AL>(a, st);
+  }
 }
 template <typename T>
 int backward_of(const LayerNormBwdArgs& a, hipStream_t st) {
   return aligned(a, (int)sizeof(typename T::S)) ? backward_al<T, true>(a, st) : backward_al<T, false>(a, st);
 }
 
-template <typename T>
-hipError_t raise_lds() {
-  const void* f[] = {(const void*)layer_norm_bwd_row<T, 1, true>,  (const void*)layer_norm_bwd_row<T, 2, true>,
-                     (const void*)layer_norm_bwd_row<T, 4, true>,  (const void*)layer_norm_bwd_row<T, 5, true>,
-                     (const void*)layer_norm_bwd_row<T, 1, false>, (const void*)layer_norm_bwd_row<T, 2, false>,
-                     (const void*)layer_norm_bwd_row<T, 4, false>, (const void*)layer_norm_bwd_row<T, 5, false>};
-  for (const void* k : f) {
+template <typename T, int NCH>
+int raise_lds() {
+  for (const void* k : {(const void*)layer_norm_bwd_row<T, NCH, true>, (const void*)layer_norm_bwd_row<T, NCH, false>}) {
     const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdLds);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess) return (int)e;
   }
-  return hipSuccess;
+  return (int)hipSuccess;
+}
+// (One piece a thread takes at most 33 KB.)
+template <typename T>
+int configure_of(int hs) {
+  switch (bwd_pieces(cdiv64(hs, vec<T>()))) {
+    case 2: return raise_lds<T, 2>();
+    case 4: return raise_lds<T, 4>();
+    case 5: return raise_lds<T, 5>();
+    default: return (int)hipSuccess;
+  }
 }
 
 }  // namespace
@@ -602,10 +617,8 @@ int launch_layer_norm_bwd(const LayerNormBwdArgs& a, int dtype, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   return dtype == 0 ? backward_of<Bf16>(a, st) : dtype == 1 ? backward_of<Fp16>(a, st) : backward_of<Fp32>(a, st);
 }
-int configure_layer_norm_kernels() {
-  for (const hipError_t e : {raise_lds<Bf16>(), raise_lds<Fp16>(), raise_lds<Fp32>()})
-    if (e != hipSuccess) return (int)e;
-  return (int)hipSuccess;
+int configure_layer_norm_kernels(int hs, int dtype) {
+  return dtype == 0 ? configure_of<Bf16>(hs) : dtype == 1 ? configure_of<Fp16>(hs) : configure_of<Fp32>(hs);
 }
 
 }  // namespace hcgr

@@ -458,12 +458,7 @@ int raise_lds() {
 
 }  // namespace
 
-// Raises the dynamic-LDS limit of the kernels on the current device.
-int configure_linear_kernels() {
-  for (int e : {raise_lds<0>(), raise_lds<1>(), raise_lds<2>()})
-    if (e != (int)hipSuccess) return e;
-  return (int)hipSuccess;
-}
+int configure_linear_kernels(int dtype) { return dtype == 0 ? raise_lds<0>() : dtype == 1 ? raise_lds<1>() : raise_lds<2>(); }
 
 int launch_linear(const LinearArgs& args, int dtype, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);

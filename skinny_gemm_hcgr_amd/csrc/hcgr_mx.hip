@@ -803,10 +803,8 @@ int launch_mx_linear(const MxLinearArgs& args, int dtype, void* stream) {
   return (int)hipSuccess;
 }
 
-int configure_mx_kernels() {
-  for (const hipError_t e : {raise_lds<0>(), raise_lds<1>(), raise_lds<2>()})
-    if (e != hipSuccess) return (int)e;
-  return (int)hipSuccess;
+int configure_mx_kernels(int dtype) {
+  return (int)(dtype == 0 ? raise_lds<0>() : dtype == 1 ? raise_lds<1>() : raise_lds<2>());
 }
 
 }  // namespace hcgr

@@ -1,6 +1,7 @@
 """What a call of the library launches, without a GPU: ``Recorder`` runs the
 library in a child process on the stand-in runtime of ``recording_runtime.cpp``
-and gives back each call's status and launches. Addresses are never
+and gives back each call's status and launches, and the dynamic-LDS limits that
+making its handle raised. Addresses are never
 dereferenced there, so calls of any size can be asked for."""
 from __future__ import annotations
 
@@ -49,8 +50,13 @@ def _answer(rt, H, q):
     cfg = getattr(H, q["config"])(**q["values"])
     kind = {"Config": "hcgr", "BlockConfig": "hcgr_block", "LinearConfig": "hcgr_linear"}[q["config"]]
     rt.hipSetDevice(0)
+    rt.forget_limits()
     handle = getattr(H, kind + "_create")(cfg, q.get("device", 0))
     try:
+        limits = []
+        for line in rt.recorded_limits().decode().splitlines():
+            value, device, name = line.split(" ", 2)
+            limits.append({"limit": int(value), "device": int(device), "kernel": name})
         rt.hipSetDevice(q.get("current", 0))
         rt.forget_launches()
         status = getattr(H, q["call"])(handle, *q["args"], stream=q.get("stream", 0), check=False)
@@ -60,14 +66,14 @@ def _answer(rt, H, q):
         for line in rt.recorded_launches().decode().splitlines():
             *n, name = line.split(" ", 9)
             launches.append({**dict(zip((*GRID, *BLOCK, "lds", "stream", "device"), map(int, n))), "kernel": name})
-        return {"status": status, "error": H.last_error(), "current": now.value, "launches": launches}
+        return {"status": status, "error": H.last_error(), "current": now.value, "launches": launches, "limits": limits}
     finally:
         getattr(H, kind + "_destroy")(handle)
 
 
 def main():
     rt = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)  # before the library, which then binds to it
-    rt.recorded_launches.restype = rt.registered_kernels.restype = ctypes.c_char_p
+    rt.recorded_launches.restype = rt.registered_kernels.restype = rt.recorded_limits.restype = ctypes.c_char_p
     sys.path.insert(0, ROOT)
     import skinny_gemm_hcgr_amd as H
     H.load_library()

@@ -1,6 +1,7 @@
 // A stand-in for the HIP runtime, for host tests: two gfx950 devices that run
 // nothing. It notes every kernel launch (name, grid, workgroup, dynamic LDS,
-// stream, current device) and hands the notes out as lines of text. Streams
+// stream, current device) and hands the notes out as lines of text, and likewise
+// the dynamic-LDS limits that were raised (limit, current device, name). Streams
 // are numbers: device * 16 + index, NULL the current device's default stream.
 #include <cxxabi.h>
 #include <hip/hip_runtime.h>
@@ -13,7 +14,7 @@
 
 namespace {
 std::map<const void*, std::string> kernels;
-std::string notes;
+std::string notes, limits;
 int current = 0;
 struct {
   dim3 grid, block;
@@ -32,6 +33,8 @@ extern "C" {
 
 const char* recorded_launches() { return notes.c_str(); }
 void forget_launches() { notes.clear(); }
+const char* recorded_limits() { return limits.c_str(); }
+void forget_limits() { limits.clear(); }
 const char* registered_kernels() {
   static std::string all;
   all.clear();
@@ -72,7 +75,11 @@ hipError_t hipExtLaunchKernel(const void* f, dim3 grid, dim3 block, void**, size
   return hipSuccess;
 }
 hipError_t hipGetLastError() { return hipSuccess; }
-hipError_t hipFuncSetAttribute(const void*, hipFuncAttribute, int) { return hipSuccess; }
+hipError_t hipFuncSetAttribute(const void* f, hipFuncAttribute a, int value) {
+  if (a == hipFuncAttributeMaxDynamicSharedMemorySize)
+    limits += std::to_string(value) + " " + std::to_string(current) + " " + kernels[f] + "\n";
+  return hipSuccess;
+}
 hipError_t hipMemset(void*, int, size_t) { return hipSuccess; }
 hipError_t hipGetSymbolAddress(void** p, const void*) {
   *p = (void*)0x10000;
