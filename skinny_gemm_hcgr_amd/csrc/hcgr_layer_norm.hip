@@ -245,8 +245,9 @@ __global__ __launch_bounds__(1024) void layer_norm_loop(LayerNormArgs a) {
 // row's products and stores, each wave's into a place of its own. Bound by
 // memory where there are rows enough: 29.3 us for 8192 rows of 2560 bf16
 // channels (4.3 TB/s of x, dxn and dx; 9.3 us are spent before the first row is
-// there and in the sums of dw and db), 55.4 us for 16384 (4.5 TB/s). Odd widths,
-// whose last pieces go one element at a time, pay for it (2563 channels: 145 us).
+// there and in the sums of dw and db), 55.4 us for 16384 (4.5 TB/s). Rows off 16
+// bytes pay for it (2563 channels: 145 us): each of a thread's loads stands behind
+// a branch of its own for the row's end, and no row is loaded ahead.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void hide(uint4& v) { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
 // Waves of a workgroup, one workgroup a CU: as many as the registers of a wave

@@ -38,9 +38,11 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, Divide d) { return (uin
 // them: half a dword of codes to a dword) one after the other, kPieces a
 // thread, all of them asked for before the first is used. A block's 32/V lanes
 // are neighbours; a row's pieces are whole blocks, so they stay together. Bound by
-// memory, or by the launch: 10240 x 2560 in bf16 11.9 us (5.6 TB/s) and back 11.5,
-// 32 x 10240 2.5 us. Four pieces a thread 12.5, 11.5 and 2.95 us, one 12.2, 11.9 and
-// 2.4.
+// memory, or by the launch: 10240 x 2560 in bf16 11.8 us and back 11.5, 32 x 10240
+// 2.5 us, each kernel again and again over three sets of rows (157 MB, which the
+// Infinity Cache holds). Four pieces a thread 12.5, 11.5 and 2.95 us, one 12.2, 11.9
+// and 2.4. In turn, over 354 MB and behind the 52 MB that the way back has just
+// written, the quantizer takes 15.4 us (4.3 TB/s) and the way back 11.3.
 constexpr int kPieces = 2;
 template <typename T, bool AL>
 __global__ __launch_bounds__(256) void mx_quantize(MxRowsToArgs a, int blocks, Divide per_row, uint32_t pieces) {
@@ -353,7 +355,8 @@ int launch_split(const MxLinearArgs& a, int nw, hipStream_t st) {
 // tile; past the last tile they are out of range and bring zeros. Measured: 8192 x
 // 10240 x 2560 115 us (3.7 PFLOP/s; the matrix cores are busy 42% of the cycles at
 // 2.07 GHz, LDS, which the fragments' reads and the loads' writes share, 58%), 8192^3
-// 255 us (4.3 PFLOP/s). Four waves of 128 x 128 take 152 us for the first; eight
+// 251 us (4.4 PFLOP/s). Outputs that are not whole pieces go to memory from the
+// products' layout, 8 bytes a row and lane: 8192 x 10239 x 2560 185 us. Four waves of 128 x 128 take 152 us for the first; eight
 // waves of 32 x 64 on a 128 x 128 tile 37 us for 31 at 1024 x 2560 x 10240.
 // ---------------------------------------------------------------------------
 constexpr int kTurn = 2048;  // a wave's LDS in the epilogue: 16 rows of 128 bytes
@@ -703,9 +706,12 @@ constexpr Cost kCosts[] = {{16, 16, 3.2, 0.096, 0.2, 0.037},  {32, 16, 3.25, 0.0
                            {192, 256, 6.0, 1.185, 5.5, 1.4},  {256, 256, 7.1, 1.36, 7.5, 1.72}};
 
 // Waves of a split kernel's workgroup: two where several workgroups share a CU
-// (10240x2560, M = 64: 7.5 us, 9.4 with four; of 64x64 tiles from 512 on, M = 128: four
-// 10.6 us, two 11.3, M = 256: 15.6 and 12.7), eight where one wave in four would
-// walk ten units or more (2560x10240, M = 1: 6.2 us, 6.5 with four).
+// (10240x2560, M = 64: 7.5 us, 9.4 with four), eight where one wave in four would
+// walk ten units or more (2560x10240, M = 1: 6.2 us, 6.5 with four). Of 64x64 tiles
+// from 512 on: 320 tiles of 10240x2560 take four waves 10.6 us and two 11.2, 512 of
+// 8192x20000, whose scales leave room for one workgroup a CU, 71 and 98; two waves
+// are the faster ones from 257 tiles on where K is between (2560x5120, M = 512: 15.8
+// us for 18.0; 8192x8192, M = 256: 22.3 for 24.6).
 inline int split_waves(int64_t tiles, int most, int k, int few) { return tiles > most ? 2 : k > 32 * 256 ? few : 4; }
 
 template <int DT>
